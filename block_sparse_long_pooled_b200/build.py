@@ -14,8 +14,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp2.so")
 CHECKED_LIB = os.path.join(HERE, "libfp2_checked.so")
-SOURCES = ["fp2_api.cu", "pool.cu", "discover.cu", "attention.cu", "fp2_noalloc.cu"]
-HEADERS = ["fp2_device.cuh", "fp2_kernels.h", "fp2_plan.h", os.path.join("..", "..", "include", "fp2.h")]
+SOURCES = ["fp2_api.cu", "pool.cu", "discover.cu", "attention.cu", "fp2_noalloc.cu", "fp2_serve.cu", "rotate.cu",
+           "decode.cu", "evict.cu"]
+HEADERS = ["fp2_device.cuh", "fp2_kernels.h", "fp2_plan.h", "serve_kernels.h",
+           os.path.join("..", "..", "include", "fp2.h")]
 
 
 def nvcc_path() -> str:

@@ -1,0 +1,1076 @@
+// Attention of drafted tokens over a KV cache (one token: a decode step), and the attention weight
+// that each cached key receives.
+//
+// Sequence r has kv_len[r] keys, the last q_len of them its drafted tokens; token i sees every key
+// before those and the drafted keys whose bit is set in its mask (no mask: those up to its own).
+//
+// Both kernels read the cache once and little else, so bytes bound them while a KV head has few
+// query rows.  The work is one axis of units (sequence, row tile, key tile), the same for every KV
+// head; kv_len lives on the device, so each CTA scans it and takes an equal share of that axis.  A
+// grid of `groups` x KV heads puts the KV heads of one share side by side in time: their rows are
+// neighbours in DRAM.  An (item = sequence, row tile) that several groups share leaves partial
+// results in scratch, and combine_kernel joins them in group order, so results do not depend on
+// timing.  One producer warp brings K/V tiles in by TMA (page by page), consumer warps run
+// mma.sync on them: a tile has 16 to 64 query rows, below the 128 of a tcgen05 tile, and the legacy
+// tensor path keeps pace with HBM up to there.
+#include "fp2_device.cuh"
+#include "fp2_kernels.h"
+#include "serve_kernels.h"
+
+namespace fp2 {
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------------ small PTX wrappers
+
+FP2_DEVICE void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+FP2_DEVICE void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FP2_DEVICE void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// c += a (16x16) * b (16x8); bf16 operands, or f16 ones for an e4m3 cache.
+template <bool F16>
+FP2_DEVICE void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <int N>
+FP2_DEVICE void consumer_sync() {  // the N consumer threads only (barrier 1)
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+FP2_DEVICE float neg_inf() { return __uint_as_float(0xFF800000u); }
+FP2_DEVICE float pos_inf() { return __uint_as_float(0x7F800000u); }
+
+// ------------------------------------------------------------------ the axis of units
+
+// Keys of sequence r, or -1 when its length is no valid one (below its drafted tokens, above
+// max_kv_len): such a sequence has one empty tile and its rows see nothing.
+FP2_DEVICE int seq_keys(const DecodeArgs& a, const DecodePlan& P, int r) {
+  const int n = a.kv_len[r];
+  return (n < P.q_off[r + 1] - P.q_off[r] || n > a.max_kv_len) ? -1 : n;
+}
+
+// Lengths into len[] and the exclusive prefix of the units per sequence into pre[0 .. num_seqs]:
+// units = row tiles (at least least_tiles) * max(1, key tiles).  The whole block reads the lengths at once (one trip to
+// memory whatever the batch), one warp adds up.  Ends with the block synchronised.
+template <int TILE>
+FP2_DEVICE void scan_units(const DecodeArgs& a, const DecodePlan& P, int rows_per_tile, int least_tiles, long long* pre,
+                           int* len, uint32_t* status) {
+  for (int r = threadIdx.x; r < P.num_seqs; r += blockDim.x) {
+    len[r] = seq_keys(a, P, r);
+    if (len[r] < 0) set_status(status, FP2_DEV_LEN_OOB);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    long long run = 0;
+    for (int base = 0; base < P.num_seqs; base += 32) {
+      const int r = base + lane;
+      long long u = 0;
+      if (r < P.num_seqs) {
+        const int rows = (P.q_off[r + 1] - P.q_off[r]) * a.G;
+        const int tiles = len[r] <= 0 ? 1 : (len[r] + TILE - 1) / TILE;
+        u = static_cast<long long>(max((rows + rows_per_tile - 1) / rows_per_tile, least_tiles)) * tiles;
+      }
+      long long inc = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (r < P.num_seqs) pre[r] = run + inc - u;
+      run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+    if (lane == 0) pre[P.num_seqs] = run;
+  }
+  __syncthreads();
+}
+
+// The CTA's status bits go to a word of its own in scratch (see serve_kernels.h); every thread
+// calls it, with nothing of the CTA's left to do.
+FP2_DEVICE void store_status(const DecodeArgs& a, const uint32_t* status) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.scratch[kStatusFirst + blockIdx.x] = *status;
+    if (blockIdx.x == 0) *reinterpret_cast<uint2*>(a.scratch) = make_uint2(0u, kStatusMagic | gridDim.x);
+  }
+}
+
+struct Piece {  // key tiles [t0, t1) of one item
+  int r, rt, t0, t1, tiles;
+};
+
+FP2_DEVICE int active_groups(long long units, int groups) {
+  return static_cast<int>(units < 1 ? 1 : (units < groups ? units : groups));
+}
+
+// The piece that starts at unit u (u < u1 <= pre[num_seqs]).
+template <int TILE>
+FP2_DEVICE Piece piece_at(const long long* pre, const int* len, int num_seqs, long long u, long long u1) {
+  int lo = 0, hi = num_seqs - 1;  // the last r with pre[r] <= u: sequences without rows have no units
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  Piece p;
+  p.r = lo;
+  p.tiles = len[lo] <= 0 ? 1 : (len[lo] + TILE - 1) / TILE;
+  const int rem = static_cast<int>(u - pre[lo]);
+  p.rt = rem / p.tiles;
+  p.t0 = rem - p.rt * p.tiles;
+  const long long left = u1 - u;
+  p.t1 = p.tiles - p.t0 <= left ? p.tiles : p.t0 + static_cast<int>(left);
+  return p;
+}
+
+// ------------------------------------------------------------------ producer
+
+// One tile (TILE keys from key j0) of K, and of V when v_off is given, into a stage: page by page,
+// boxes of 128 bytes x up to 64 rows.  Called by a whole warp; the page ids of 32 pages at a time
+// sit in the lanes.  Returns through *valid (64 bits a word) which rows hold a key of the sequence:
+// rows past its end and rows of a page id out of range do not.
+template <int TILE, int ELT, int D>
+struct Producer {
+  static constexpr int HALVES = D * ELT / 128;            // boxes side by side
+  int page_base = -1, page_id = -1, seq = -1;             // lanes hold pages page_base .. + 31 of sequence seq
+
+  FP2_DEVICE void load(const DecodeArgs& a, const Piece& p, int keys, int g, int j0, uint32_t k_smem, uint32_t v_smem,
+                       uint64_t* bar, uint64_t* valid, uint32_t* status, bool withhold) {
+    const int lane = threadIdx.x & 31;
+    const bool paged = a.page_table != nullptr;
+    const int step = paged && a.page_size < 64 ? a.page_size : 64;
+    const int end = keys < j0 + TILE ? keys : j0 + TILE;
+    uint64_t ok[TILE / 64];
+#pragma unroll
+    for (int w = 0; w < TILE / 64; ++w) ok[w] = 0;
+    uint32_t bytes = 0;
+    // First the boxes are counted, then the barrier is armed, then they are issued.
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int j = j0; j < end; j += step) {
+        int outer = p.r, row = j;
+        if (paged) {
+          const int pg = j / a.page_size;
+          row = j - pg * a.page_size;
+          if (seq != p.r || pg < page_base || pg >= page_base + 32) {
+            seq = p.r;
+            page_base = pg;
+            const int mine = pg + lane;
+            page_id = mine < (keys + a.page_size - 1) / a.page_size
+                          ? a.page_table[static_cast<int64_t>(p.r) * a.max_pages + mine]
+                          : -1;
+          }
+          outer = __shfl_sync(0xFFFFFFFFu, page_id, pg - page_base);
+          if (outer < 0 || outer >= a.num_pages) {
+            if (pass == 0 && lane == 0) set_status(status, FP2_DEV_PAGE_OOB);
+            continue;
+          }
+        }
+        if (pass == 0) {
+          const int n = end - j < step ? end - j : step;
+          const uint64_t m = (n == 64 ? ~0ull : (1ull << n) - 1) << ((j - j0) & 63);
+#pragma unroll
+          for (int w = 0; w < TILE / 64; ++w)
+            if (((j - j0) >> 6) == w) ok[w] |= m;
+          bytes += step * D * ELT * (v_smem != 0 ? 2 : 1);
+        } else if (lane == 0 && !withhold) {
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            const uint32_t off = h * (TILE * 128) + (j - j0) * 128;
+            tma_load_4d(k_smem + off, &a.tm_k, bar, h * (128 / ELT), g, row, outer);
+            if (v_smem != 0) tma_load_4d(v_smem + off, &a.tm_v, bar, h * (128 / ELT), g, row, outer);
+          }
+        }
+      }
+      if (pass == 0 && lane == 0) {
+#pragma unroll
+        for (int w = 0; w < TILE / 64; ++w) valid[w] = ok[w];
+        if (bytes != 0)
+          mbar_arrive_expect_tx(bar, bytes);
+        else
+          mbar_arrive(bar);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ operand fragments
+
+// Address of 16-byte chunk c (of the D * ELT / 16 of a row) of row k in a K/V tile: boxes of 128
+// bytes side by side, each with the 128-byte swizzle.
+template <int TILE>
+FP2_DEVICE uint32_t tile_addr(uint32_t base, int k, int c) {
+  return base + (c >> 3) * (TILE * 128) + k * 128 + (((c & 7) ^ (k & 7)) << 4);
+}
+
+// e4m3 fragments.  ldmatrix moves units of 16 bits, here two neighbouring values of d.  For QK^T the
+// order of d inside a group of 16 is free as long as Q agrees: a thread's four values 4q .. 4q+3
+// (q = lane % 4) serve as k = 2q, 2q+1 and 2q+8, 2q+9, and stage_q stores Q in that order.  For PV
+// the transposed unit holds d = 2n, 2n+1 of two keys; the bytes are regrouped by key into one
+// fragment of the even d and one of the odd d.
+FP2_DEVICE void widen_k(uint32_t w, uint32_t& b0, uint32_t& b1) {
+  b0 = e4m3x2_to_f16x2(w & 0xFFFFu);
+  b1 = e4m3x2_to_f16x2(w >> 16);
+}
+FP2_DEVICE void widen_v(uint32_t w, uint32_t& even, uint32_t& odd) {
+  const uint32_t t = __byte_perm(w, 0, 0x3120);
+  even = e4m3x2_to_f16x2(t & 0xFFFFu);
+  odd = e4m3x2_to_f16x2(t >> 16);
+}
+
+// Query rows [row0, row0 + n) of (tokens from t0, KV head g) into shared memory as 16-bit operands,
+// 16-byte chunks swizzled by row; rows from `rows` on are zero.
+template <int DT, int D>
+FP2_DEVICE uint32_t q_addr(uint32_t base, int row, int c) {
+  return base + row * (D * 2) + ((c ^ (row & 7)) << 4);
+}
+template <int DT, int D, int NTHREADS>
+FP2_DEVICE void stage_q(const DecodeArgs& a, char* q_smem, int t0, int g, int row0, int n, int rows, int tid) {
+  constexpr int CH = D / 8;  // 16-byte chunks of a 16-bit row
+  for (int i = tid; i < n * CH; i += NTHREADS) {
+    const int rr = i / CH, c = i - rr * CH, m = row0 + rr;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (m < rows) {
+      const int tok = m / a.G, h = g * a.G + (m - tok * a.G);
+      const int64_t e = (static_cast<int64_t>(t0) + tok) * a.q_stride + static_cast<int64_t>(h) * D;
+      if constexpr (DT == 1) {
+        v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + e + 8 * c);
+      } else {
+        // chunk c holds k = 8 (c % 2) .. + 7 of group c / 2: values 4q + 2 (c % 2), + 1 for q = 0 .. 3
+        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + e + 16 * (c >> 1));
+        const uint32_t s = (c & 1) * 16;
+        v.x = e4m3x2_to_f16x2((w.x >> s) & 0xFFFFu);
+        v.y = e4m3x2_to_f16x2((w.y >> s) & 0xFFFFu);
+        v.z = e4m3x2_to_f16x2((w.z >> s) & 0xFFFFu);
+        v.w = e4m3x2_to_f16x2((w.w >> s) & 0xFFFFu);
+      }
+    }
+    *reinterpret_cast<uint4*>(q_smem + rr * (D * 2) + ((c ^ (rr & 7)) << 4)) = v;
+  }
+}
+
+// Which of the 16 keys from key j a token sees, bit by bit: all below `base` (the first drafted
+// key), of the drafted ones those in its mask.
+FP2_DEVICE uint32_t seen16(uint64_t mask, int j, int base) {
+  const int off = j - base;
+  if (off >= 0) return off < 64 ? static_cast<uint32_t>(mask >> off) & 0xFFFFu : 0u;
+  if (off <= -16) return 0xFFFFu;
+  return static_cast<uint32_t>((mask << -off) | ((1ull << -off) - 1)) & 0xFFFFu;
+}
+FP2_DEVICE uint64_t token_mask(const DecodeArgs& a, int t0, int i) {
+  return a.mask != nullptr ? a.mask[static_cast<int64_t>(t0) + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
+}
+
+// ------------------------------------------------------------------ tree attention
+
+// Rows of a CTA: WM warps x MT tiles of 16; the 64 keys of a tile go to 4 warps, 16 each.
+template <int DT, int D, int MT, int WM>
+struct Tree {
+  static constexpr int ELT = DT == 1 ? 2 : 1;
+  static constexpr bool F16 = DT == 2;
+  static constexpr int WN = 4, TILE = kTreeTile;
+  static constexpr int ROWS = 16 * MT * WM;
+  static constexpr int CONSUMERS = 32 * WM * WN;
+  static constexpr int THREADS = CONSUMERS + 32;
+  static constexpr int KV_BYTES = TILE * D * ELT;               // one of K or V
+  static constexpr int STAGE_BYTES = 2 * KV_BYTES;
+  static constexpr int Q_BYTES = ROWS * D * 2;
+  static constexpr int OS = D + 8;                              // row stride of the joined output, floats
+  static constexpr int O_BYTES = ROWS * OS * 4;
+  static constexpr int FIXED = 1024 /* alignment */ + Q_BYTES + O_BYTES + WN * ROWS * 8 + (FP2_MAX_SEQS + 1) * 8 +
+                               FP2_MAX_SEQS * 4 + 256;
+  static constexpr int CTAS = ROWS <= 32 ? 2 : 1;               // per SM
+  static constexpr int BUDGET = CTAS == 2 ? 113 * 1024 : 226 * 1024;
+  static constexpr int RAW = (BUDGET - FIXED) / STAGE_BYTES;
+  static constexpr int STAGES = RAW > 8 ? 8 : RAW;
+  static constexpr int SMEM = FIXED + STAGES * STAGE_BYTES;
+  // P is held in bf16 against a bf16 V.  Its rounding (2^-9 of each weight) would be as large as the
+  // output's own; where few rows leave the tensor cores idle a second product adds the remainder
+  // P - bf16(P), which costs nothing measurable there.
+  static constexpr bool SPLIT_P = DT == 1 && ROWS <= 32;
+  // e4m3: P is f16, scaled by 2^8 so that weights down to 2^-22 of the largest keep all 11 bits; the
+  // factor leaves with the division by the sum.
+  static constexpr float P_BIAS = F16 ? 8.f : 0.f;
+};
+
+template <int DT, int D, int MT, int WM>
+__global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, WM>::CTAS)
+    tree_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P) {
+  using C = Tree<DT, D, MT, WM>;
+  extern __shared__ char smem_raw[];
+  char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  char* stages = smem;
+  char* q_smem = stages + C::STAGES * C::STAGE_BYTES;
+  float* o_smem = reinterpret_cast<float*>(q_smem + C::Q_BYTES);
+  float2* ml_smem = reinterpret_cast<float2*>(reinterpret_cast<char*>(o_smem) + C::O_BYTES);  // [WN][ROWS]
+  long long* pre = reinterpret_cast<long long*>(ml_smem + C::WN * C::ROWS);
+  int* len = reinterpret_cast<int*>(pre + FP2_MAX_SEQS + 1);
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], valid[C::STAGES];
+  __shared__ int abort_flag;
+  __shared__ uint32_t status_word;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], C::CONSUMERS / 32);
+    }
+    abort_flag = 0;
+    status_word = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&a.tm_k);
+    tma_prefetch_desc(&a.tm_v);
+  }
+  __syncthreads();
+  scan_units<C::TILE>(a, P, C::ROWS, 0, pre, len, &status_word);
+  const long long units = pre[P.num_seqs];
+  const int ng = active_groups(units, a.groups);
+  if (grp >= ng) {
+    if (g == 0 && tid == 0) a.desc[grp] = make_int4(-1, 0, 0, 0);
+    store_status(a, &status_word);
+    return;
+  }
+  const long long u0 = units * grp / ng, u1 = units * (grp + 1) / ng;
+
+  if (warp == C::CONSUMERS / 32) {
+    // ---------------- producer
+    Producer<C::TILE, C::ELT, D> load;
+    int s = 0, it = 0;
+    for (long long u = u0; u < u1;) {
+      const Piece p = piece_at<C::TILE>(pre, len, P.num_seqs, u, u1);
+      for (int t = p.t0; t < p.t1; ++t) {
+        if (it >= C::STAGES) {
+          // One answer for the warp: lanes that gave up and lanes that did not would wait for each other.
+          const bool free = mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, &abort_flag, &status_word, a.wait_limit_ns);
+          if (!__all_sync(0xFFFFFFFFu, free)) goto drain;
+        }
+        const uint32_t k_at = smem_u32(stages + s * C::STAGE_BYTES);
+        load.load(a, p, len[p.r], g, t * C::TILE, k_at, k_at + C::KV_BYTES, &full[s], &valid[s],
+                  &status_word, it == a.withhold);
+        ++it;
+        if (++s == C::STAGES) s = 0;
+      }
+      u += p.t1 - p.t0;
+    }
+  drain:
+    // Copies in flight end before the CTA does: the consumers have waited for every tile, unless
+    // they gave up, and then the issued ones are waited for here, within a fifth of the limit.
+    if (*static_cast<volatile int*>(&abort_flag)) {
+      volatile int no_abort = 0;
+      for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+        mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, &status_word, a.wait_limit_ns / 5);
+    }
+    store_status(a, &status_word);
+    return;
+  }
+
+  // ---------------- consumers
+  const int wm = warp / C::WN, wn = warp % C::WN;
+  const uint32_t q_base = smem_u32(q_smem);
+  int s = 0, it = 0, nth = 0;
+  bool alive = true;
+  for (long long u = u0; u < u1; ++nth) {
+    const Piece p = piece_at<C::TILE>(pre, len, P.num_seqs, u, u1);
+    const int keys = len[p.r], t0 = P.q_off[p.r], q_len = P.q_off[p.r + 1] - t0;
+    const int row0 = p.rt * C::ROWS, rows = q_len * a.G;
+    const int base = keys - q_len;  // first drafted key
+    consumer_sync<C::CONSUMERS>();  // the previous piece is written: q_smem, o_smem and ml_smem are free
+    stage_q<DT, D, C::CONSUMERS>(a, q_smem, t0, g, row0, C::ROWS, rows, tid);
+    consumer_sync<C::CONSUMERS>();
+    // For one row tile of 16 the query fragments stay in registers; two would not fit next to O.
+    uint32_t qf[MT == 1 ? D / 16 : 1][4];
+    if constexpr (MT == 1) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        ldsm4(q_addr<DT, D>(q_base, wm * 16 + (lane & 15), 2 * k + (lane >> 4)), qf[k]);
+    }
+    float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      mx[m][0] = mx[m][1] = neg_inf();
+      sum[m][0] = sum[m][1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
+    }
+
+    for (int t = p.t0; t < p.t1; ++t) {
+      if (alive) alive = mbar_wait(&full[s], (it / C::STAGES) & 1, &abort_flag, &status_word, a.wait_limit_ns);
+      if (!__all_sync(0xFFFFFFFFu, alive)) {
+        alive = false;
+        ++it;
+        if (++s == C::STAGES) s = 0;
+        continue;
+      }
+      const uint32_t k_at = smem_u32(stages + s * C::STAGE_BYTES), v_at = k_at + C::KV_BYTES;
+      const int j0 = t * C::TILE + wn * 16;             // first of this warp's 16 keys
+      const uint32_t here = static_cast<uint32_t>(valid[s] >> (wn * 16)) & 0xFFFFu;
+      // Rows differ in what they see only from the first drafted key on.
+      const bool plain = here == 0xFFFFu && j0 + 16 <= base;
+
+      // S = Q K^T, 16 rows x 16 keys per row tile
+      float sc[MT][2][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) sc[m][n][0] = sc[m][n][1] = sc[m][n][2] = sc[m][n][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        if constexpr (!C::F16) {
+          ldsm4(tile_addr<C::TILE>(k_at, wn * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b);
+        } else {
+          if ((k & 1) == 0) continue;  // two groups of 16 values at a time, below
+        }
+        if constexpr (!C::F16) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            uint32_t q4[4];
+            const uint32_t(&qa)[4] = MT == 1 ? qf[k * (MT == 1)] : q4;
+            if constexpr (MT != 1)
+              ldsm4(q_addr<DT, D>(q_base, (wm * MT + m) * 16 + (lane & 15), 2 * k + (lane >> 4)), q4);
+            mma<false>(sc[m][0], qa, b[0], b[1]);
+            mma<false>(sc[m][1], qa, b[2], b[3]);
+          }
+        } else {
+          // matrices: keys 0-7 and 8-15 of chunk k - 1, then of chunk k
+          ldsm4(tile_addr<C::TILE>(k_at, wn * 16 + (lane & 15), k - 1 + (lane >> 4)), b);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t b00, b01, b10, b11;
+            widen_k(b[2 * c], b00, b01);
+            widen_k(b[2 * c + 1], b10, b11);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              uint32_t q4[4];
+              const uint32_t(&qa)[4] = MT == 1 ? qf[(k - 1 + c) * (MT == 1)] : q4;
+              if constexpr (MT != 1)
+                ldsm4(q_addr<DT, D>(q_base, (wm * MT + m) * 16 + (lane & 15), 2 * (k - 1 + c) + (lane >> 4)), q4);
+              mma<true>(sc[m][0], qa, b00, b01);
+              mma<true>(sc[m][1], qa, b10, b11);
+            }
+          }
+        }
+      }
+
+      // Masks, the running maximum and the weights
+      uint32_t pf[MT][4], pl[MT][4];
+      uint32_t vis[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        vis[m][0] = vis[m][1] = here;
+        if (!plain) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = row0 + (wm * MT + m) * 16 + (lane >> 2) + 8 * i;
+            vis[m][i] = row < rows && keys > 0 ? here & seen16(token_mask(a, t0, row / a.G), j0, base) : 0u;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!((vis[m][i] >> (8 * n + 2 * (lane & 3) + e)) & 1u)) sc[m][n][2 * i + e] = neg_inf();
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v = fmaxf(fmaxf(sc[m][0][2 * i], sc[m][0][2 * i + 1]), fmaxf(sc[m][1][2 * i], sc[m][1][2 * i + 1]));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+          const float now = fmaxf(mx[m][i], v);
+          if (__any_sync(0xFFFFFFFFu, now > mx[m][i])) {
+            // exp2(-inf) = 0 clears a row that had seen nothing; a row that still has keeps its zeros.
+            const float f = now == neg_inf() ? 1.f : fast_exp2((mx[m][i] - now) * a.scale_log2);
+            sum[m][i] *= f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              o[m][n][2 * i] *= f;
+              o[m][n][2 * i + 1] *= f;
+            }
+            mx[m][i] = now;
+          }
+          const float off = now == neg_inf() ? 0.f : C::P_BIAS - now * a.scale_log2;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float e0 = fast_exp2(fmaf(sc[m][n][2 * i], a.scale_log2, off));
+            const float e1 = fast_exp2(fmaf(sc[m][n][2 * i + 1], a.scale_log2, off));
+            sum[m][i] += e0 + e1;
+            const uint32_t w = C::F16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+            pf[m][2 * n + i] = w;
+            if constexpr (C::SPLIT_P)
+              pl[m][2 * n + i] = pack_bf16x2(e0 - __uint_as_float(w << 16), e1 - __uint_as_float(w & 0xFFFF0000u));
+          }
+        }
+      }
+
+      // O += P V.  Rows of V that hold no key are cleared (0 x NaN is NaN).  A drafted key's row that
+      // is not finite would reach rows that do not see it the same way: its values are cleared too and
+      // added afterwards to the rows that do see the key.
+      uint32_t clr[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (!plain) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t two = here >> (2 * (lane & 3) + 8 * i);
+          clr[i] = ((two & 1u) ? 0xFFFFu : 0u) | ((two & 2u) ? 0xFFFF0000u : 0u);
+        }
+      }
+      const auto pv = [&](int n, uint32_t b0, uint32_t b1) {  // accumulator n, keys 0-7 and 8-15 of the warp's 16
+        if (!plain) {
+          b0 &= clr[0];
+          b1 &= clr[1];
+          constexpr uint32_t EXP = C::F16 ? 0x7C00u : 0x7F80u;
+          const uint32_t b[2] = {b0, b1};
+          uint32_t bad[4];
+          bool any = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t h = (b[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+            bad[e] = (h & EXP) == EXP ? h : 0u;
+            any |= bad[e] != 0;
+          }
+          if (__any_sync(0xFFFFFFFFu, any)) {
+            // How many seen keys of each row hold +inf, -inf or NaN, as products of 0/1 operands.
+            constexpr uint32_t ONE = C::F16 ? 0x3C00u : 0x3F80u;
+            if (bad[0]) b0 &= 0xFFFF0000u;
+            if (bad[1]) b0 &= 0xFFFFu;
+            if (bad[2]) b1 &= 0xFFFF0000u;
+            if (bad[3]) b1 &= 0xFFFFu;
+#pragma unroll
+            for (int kind = 0; kind < 3; ++kind) {
+              uint32_t f[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                f[e] = (kind == 0 ? bad[e] == EXP : kind == 1 ? bad[e] == (EXP | 0x8000u) : (bad[e] & 0x7FFFu) > EXP)
+                           ? ONE : 0u;
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                uint32_t va[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t two = vis[m][e & 1] >> (2 * (lane & 3) + 8 * (e >> 1));
+                  va[e] = ((two & 1u) ? ONE : 0u) | ((two & 2u) ? ONE << 16 : 0u);
+                }
+                float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+                mma<C::F16>(cnt, va, f[0] | (f[1] << 16), f[2] | (f[3] << 16));
+                const float add = kind == 0 ? pos_inf() : kind == 1 ? neg_inf() : __uint_as_float(0x7FFFFFFFu);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (cnt[e] > 0.f) o[m][n][e] += add;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          mma<C::F16>(o[m][n], pf[m], b0, b1);
+          if constexpr (C::SPLIT_P) mma<C::F16>(o[m][n], pl[m], b0, b1);
+        }
+      };
+      if constexpr (!C::F16) {
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t b[4];
+          ldsm4t(tile_addr<C::TILE>(v_at, wn * 16 + (lane & 15), 2 * n + (lane >> 4)), b);
+          pv(2 * n, b[0], b[1]);
+          pv(2 * n + 1, b[2], b[3]);
+        }
+      } else {
+        // a 16-byte chunk is 16 values of d: accumulator 2c takes its even ones, 2c + 1 its odd ones
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) {
+          uint32_t b[4], even[4], odd[4];
+          ldsm4t(tile_addr<C::TILE>(v_at, wn * 16 + (lane & 15), 2 * n + (lane >> 4)), b);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) widen_v(b[e], even[e], odd[e]);
+          pv(4 * n, even[0], even[1]);
+          pv(4 * n + 1, odd[0], odd[1]);
+          pv(4 * n + 2, even[2], even[3]);
+          pv(4 * n + 3, odd[2], odd[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      ++it;
+      if (++s == C::STAGES) s = 0;
+    }
+
+    // Join the four key warps of each row: agree on the maximum, then add O up in warp order.
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = sum[m][i];
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+        if ((lane & 3) == 0)
+          ml_smem[wn * C::ROWS + (wm * MT + m) * 16 + (lane >> 2) + 8 * i] = make_float2(mx[m][i], x);
+      }
+    consumer_sync<C::CONSUMERS>();
+    float fac[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = (wm * MT + m) * 16 + (lane >> 2) + 8 * i;
+        float top = neg_inf();
+#pragma unroll
+        for (int w = 0; w < C::WN; ++w) top = fmaxf(top, ml_smem[w * C::ROWS + row].x);
+        fac[m][i] = mx[m][i] == neg_inf() ? 0.f : fast_exp2((mx[m][i] - top) * a.scale_log2);
+      }
+    for (int w = 0; w < C::WN; ++w) {
+      if (w == wn) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float* dst = o_smem + ((wm * MT + m) * 16 + (lane >> 2) + 8 * i) * C::OS;
+            const float f = fac[m][i];
+            if constexpr (!C::F16) {
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                float2* at = reinterpret_cast<float2*>(dst + 8 * n + 2 * (lane & 3));
+                float2 old = w == 0 ? make_float2(0.f, 0.f) : *at;
+                // a row this warp saw nothing of adds nothing (its accumulators are zero)
+                old.x += o[m][n][2 * i] * f;
+                old.y += o[m][n][2 * i + 1] * f;
+                *at = old;
+              }
+            } else {
+              // columns 2q, 2q+1 of the even and odd accumulators are d = 4q, 4q+2 and 4q+1, 4q+3
+#pragma unroll
+              for (int n = 0; n < D / 16; ++n) {
+                float4* at = reinterpret_cast<float4*>(dst + 16 * n + 4 * (lane & 3));
+                float4 old = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *at;
+                old.x += o[m][2 * n][2 * i] * f;
+                old.y += o[m][2 * n + 1][2 * i] * f;
+                old.z += o[m][2 * n][2 * i + 1] * f;
+                old.w += o[m][2 * n + 1][2 * i + 1] * f;
+                *at = old;
+              }
+            }
+          }
+      }
+      consumer_sync<C::CONSUMERS>();
+    }
+
+    // Out: the whole item, or this group's part of it.
+    const bool whole = p.t0 == 0 && p.t1 == p.tiles;
+    const int slot = (grp * a.Hkv + g) * 2 + (nth == 0 ? 0 : 1);
+    constexpr int LANES = D / 4;  // threads of a row, four values each
+    for (int i = tid; i < C::ROWS * LANES; i += C::CONSUMERS) {
+      const int rr = i / LANES, c = (i - rr * LANES) * 4, m = row0 + rr;
+      if (m >= rows) continue;
+      float top = neg_inf(), total = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::WN; ++w) top = fmaxf(top, ml_smem[w * C::ROWS + rr].x);
+#pragma unroll
+      for (int w = 0; w < C::WN; ++w) {
+        const float2 x = ml_smem[w * C::ROWS + rr];
+        // a warp that saw nothing has the sum 0; one whose scores are all NaN has the maximum -inf too
+        total += x.y == 0.f ? 0.f : x.y * fast_exp2((x.x - top) * a.scale_log2);
+      }
+      const float4 v = *reinterpret_cast<const float4*>(o_smem + rr * C::OS + c);
+      if (whole) {
+        const int tok = m / a.G, h = g * a.G + (m - tok * a.G);
+        const float f = total == 0.f ? 0.f : a.v_descale / total;
+        const int64_t row = static_cast<int64_t>(t0) + tok;
+        if (fp2_check(row < a.T && h < a.Hq, &status_word)) {
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (row * a.Hq + h) * D + c) =
+              make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+          if (c == 0 && a.lse != nullptr)
+            a.lse[static_cast<int64_t>(h) * a.T + row] =
+                total == 0.f ? neg_inf() : (top * a.scale_log2 - C::P_BIAS + log2f(total)) * kLn2;
+        }
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * C::ROWS + rr) * D + c) = v;
+        if (c == 0)
+          a.part_ml[static_cast<int64_t>(slot) * C::ROWS + rr] =
+              make_float2(top == neg_inf() ? top : top * a.scale_log2 - C::P_BIAS, total);
+      }
+    }
+    // The group that holds an item's first piece tells combine_kernel how many follow.
+    u += p.t1 - p.t0;
+    if (g == 0 && tid == 0 && u >= u1) {
+      int4 d = make_int4(-1, 0, 0, 0);
+      if (p.t0 == 0 && p.t1 < p.tiles) {
+        const long long last = u1 + (p.tiles - p.t1) - 1;  // the item's last unit
+        int e = grp + 1;
+        while (units * (e + 1) / ng <= last) ++e;
+        d = make_int4(nth == 0 ? 0 : 1, p.r, p.rt, e - grp + 1);
+      }
+      a.desc[grp] = d;
+    }
+  }
+  store_status(a, &status_word);
+}
+
+// Joins the pieces of an item that several groups worked on, in group order: one warp per row,
+// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ DecodeArgs a,
+                                                      const __grid_constant__ DecodePlan P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
+  const int4 d = a.desc[grp];
+  if (d.x < 0) return;
+  const int rr = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int t0 = P.q_off[d.y], rows = (P.q_off[d.y + 1] - t0) * a.G, m = d.z * ROWS + rr;
+  if (m >= rows) return;
+  const auto at = [&](int i) {  // row of piece i in the partial buffers
+    const int64_t slot = (static_cast<int64_t>(grp + i) * a.Hkv + g) * 2 + (i == 0 ? d.x : 0);
+    return slot * ROWS + rr;
+  };
+  float top = neg_inf();
+  bool any = false;  // some piece saw a key (all of whose scores may be NaN)
+  for (int i = lane; i < d.w; i += 32) {
+    const float2 ml = a.part_ml[at(i)];
+    top = fmaxf(top, ml.x);
+    any |= !(ml.y == 0.f);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  constexpr int V = D / 32;
+  float acc[V], total = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  if (__any_sync(0xFFFFFFFFu, any)) {
+#pragma unroll 8
+    for (int i = 0; i < d.w; ++i) {
+      const int64_t row = at(i);
+      const float2 ml = a.part_ml[row];
+      const float w = ml.y == 0.f ? 0.f : fast_exp2(ml.x - top);
+      total += w * ml.y;
+      const float* src = a.part_o + row * D + lane * V;
+      float x[V];
+      if constexpr (V == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        x[0] = v.x, x[1] = v.y;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += w * x[e];
+    }
+  }
+  const int tok = m / a.G, h = g * a.G + (m - tok * a.G);
+  const int64_t row = static_cast<int64_t>(t0) + tok;
+  const float f = total == 0.f ? 0.f : a.v_descale / total;
+  // the word of the attention CTA with this index, written before this kernel went on
+  if (!fp2_check(row < a.T && h < a.Hq, a.scratch + kStatusFirst + blockIdx.x)) return;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (row * a.Hq + h) * D + lane * V);
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * f, acc[2 * e + 1] * f);
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[static_cast<int64_t>(h) * a.T + row] = total == 0.f ? neg_inf() : (top + log2f(total)) * kLn2;
+}
+
+template <int DT, int D, int MT, int WM>
+cudaError_t run_tree(const DecodeArgs& a, const DecodePlan& P, int max_rows, cudaStream_t stream) {
+  using C = Tree<DT, D, MT, WM>;
+  static_assert(C::STAGES >= 2, "tiles must fit twice");
+  const auto kernel = tree_kernel<DT, D, MT, WM>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
+  if (e != cudaSuccess) return e;
+  kernel<<<a.groups * a.Hkv, C::THREADS, C::SMEM, stream>>>(a, P);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.groups == 1) return cudaSuccess;  // no item is split
+  // Launched while the attention still runs; griddepcontrol.wait holds it until that has ended.
+  cudaLaunchConfig_t cfg{};
+  const int rows = max_rows < C::ROWS ? max_rows : C::ROWS;
+  cfg.gridDim = dim3(a.groups * a.Hkv, (rows + 3) / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D, C::ROWS>, a, P);
+}
+
+template <int DT, int D>
+cudaError_t run_tree_rows(const DecodeArgs& a, const DecodePlan& P, int max_rows, cudaStream_t stream) {
+  switch (tree_rows(max_rows)) {
+    case 16: return run_tree<DT, D, 1, 1>(a, P, max_rows, stream);
+    case 32: return run_tree<DT, D, 2, 1>(a, P, max_rows, stream);
+    default: return run_tree<DT, D, 2, 2>(a, P, max_rows, stream);
+  }
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ key mass
+
+namespace {
+
+template <int DT, int D>
+struct Mass {
+  static constexpr int ELT = DT == 1 ? 2 : 1;
+  static constexpr bool F16 = DT == 2;
+  static constexpr int TILE = kMassTile, WARPS = 4, CONSUMERS = 32 * WARPS, THREADS = CONSUMERS + 32;
+  static constexpr int STAGE_BYTES = TILE * D * ELT;
+  static constexpr int BUDGET = 113 * 1024;  // two CTAs per SM
+  static constexpr int MAX_STAGES = 6;
+  // Query rows (16-bit, and 8 bytes of statistics) held at once; the rest comes in further passes.
+  static constexpr int fixed(int q_rows) {
+    return 1024 + q_rows * (D * 2 + 8) + (FP2_MAX_SEQS + 1) * 8 + FP2_MAX_SEQS * 4 + 256;
+  }
+  static constexpr int stages(int q_rows) {
+    const int n = (BUDGET - fixed(q_rows)) / STAGE_BYTES;
+    return n > MAX_STAGES ? MAX_STAGES : n;
+  }
+};
+
+// mass'[r, g, j] = decay * mass[r, g, j] + sum over the rows that see key j of exp(q.k_j scale - lse).
+// A CTA owns whole key tiles (all query rows of the head), so every sum is one thread group's, in
+// row order: no atomics.  Four warps, 32 keys each; the K fragments of a warp's keys stay in
+// registers while it walks the query rows in shared memory.
+template <int DT, int D>
+__global__ void __launch_bounds__(Mass<DT, D>::THREADS, 2)
+    mass_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P, int stages) {
+  using C = Mass<DT, D>;
+  extern __shared__ char smem_raw[];
+  char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  char* ring = smem;
+  char* q_smem = ring + stages * C::STAGE_BYTES;
+  float* neg_lse = reinterpret_cast<float*>(q_smem + a.q_rows * D * 2);  // [q_rows] -lse in log2 units
+  long long* pre = reinterpret_cast<long long*>(neg_lse + 2 * a.q_rows);
+  int* len = reinterpret_cast<int*>(pre + FP2_MAX_SEQS + 1);
+  __shared__ uint64_t full[C::MAX_STAGES], empty[C::MAX_STAGES], valid[C::MAX_STAGES][2];
+  __shared__ int abort_flag;
+  __shared__ uint32_t status_word;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], C::WARPS);
+    }
+    abort_flag = 0;
+    status_word = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&a.tm_k);
+  }
+  __syncthreads();
+  // All rows of a (sequence, head) count as one row tile, no rows too (its weights still decay):
+  // units are key tiles.
+  scan_units<C::TILE>(a, P, FP2_MAX_DRAFT * a.G, 1, pre, len, &status_word);
+  const long long units = pre[P.num_seqs];
+  const int ng = active_groups(units, a.groups);
+  if (grp >= ng) {
+    store_status(a, &status_word);
+    return;
+  }
+  const long long u0 = units * grp / ng, u1 = units * (grp + 1) / ng;
+
+  if (warp == C::WARPS) {
+    Producer<C::TILE, C::ELT, D> load;
+    int s = 0, it = 0;
+    for (long long u = u0; u < u1;) {
+      const Piece p = piece_at<C::TILE>(pre, len, P.num_seqs, u, u1);
+      const int rows = (P.q_off[p.r + 1] - P.q_off[p.r]) * a.G;
+      for (int c0 = 0; c0 == 0 || c0 < rows; c0 += a.q_rows) {
+        for (int t = p.t0; t < p.t1; ++t) {
+          if (it >= stages) {
+            const bool free = mbar_wait(&empty[s], ((it / stages) & 1) ^ 1, &abort_flag, &status_word, a.wait_limit_ns);
+            if (!__all_sync(0xFFFFFFFFu, free)) goto drain;
+          }
+          load.load(a, p, len[p.r], g, t * C::TILE, smem_u32(ring + s * C::STAGE_BYTES), 0, &full[s], valid[s],
+                    &status_word, it == a.withhold);
+          ++it;
+          if (++s == stages) s = 0;
+        }
+      }
+      u += p.t1 - p.t0;
+    }
+  drain:
+    if (*static_cast<volatile int*>(&abort_flag)) {
+      volatile int no_abort = 0;
+      for (int i = it > stages ? it - stages : 0; i < it; ++i)
+        mbar_wait(&full[i % stages], (i / stages) & 1, &no_abort, &status_word, a.wait_limit_ns / 5);
+    }
+    store_status(a, &status_word);
+    return;
+  }
+
+  const uint32_t q_base = smem_u32(q_smem);
+  int s = 0, it = 0;
+  bool alive = true;
+  for (long long u = u0; u < u1;) {
+    const Piece p = piece_at<C::TILE>(pre, len, P.num_seqs, u, u1);
+    const int keys = len[p.r], t0 = P.q_off[p.r], q_len = P.q_off[p.r + 1] - t0;
+    const int rows = q_len * a.G, base = keys - q_len;
+    const int had = a.mass_in == nullptr ? 0 : (a.mass_len != nullptr ? a.mass_len[p.r] : keys);
+    for (int c0 = 0; c0 == 0 || c0 < rows; c0 += a.q_rows) {
+      const int n_rows = min(a.q_rows, rows - c0), n16 = (n_rows + 15) / 16;
+      consumer_sync<C::CONSUMERS>();  // every warp is done with the rows before
+      stage_q<DT, D, C::CONSUMERS>(a, q_smem, t0, g, c0, n16 * 16, rows, tid);
+      for (int i = tid; i < n16 * 16; i += C::CONSUMERS) {
+        float x = neg_inf();  // rows that are none, or saw nothing: 2^-inf
+        if (c0 + i < rows) {
+          const int tok = (c0 + i) / a.G, h = g * a.G + (c0 + i - tok * a.G);
+          const float l = a.lse_in[static_cast<int64_t>(h) * a.T + t0 + tok];
+          if (l != neg_inf()) x = -l * 1.4426950408889634f;
+        }
+        neg_lse[i] = x;
+      }
+      consumer_sync<C::CONSUMERS>();
+
+      for (int t = p.t0; t < p.t1; ++t) {
+        if (alive) alive = mbar_wait(&full[s], (it / stages) & 1, &abort_flag, &status_word, a.wait_limit_ns);
+        if (!__all_sync(0xFFFFFFFFu, alive)) {
+          alive = false;
+          ++it;
+          if (++s == stages) s = 0;
+          continue;
+        }
+        const uint32_t k_at = smem_u32(ring + s * C::STAGE_BYTES);
+        const int kw = warp * 32, j0 = t * C::TILE + kw;
+        const uint32_t here = static_cast<uint32_t>(valid[s][warp >> 1] >> ((warp & 1) * 32));
+        // K fragments of 32 keys: [group of 16 values][group of 8 keys]
+        uint32_t kf[D / 16][4][2];
+        if constexpr (!C::F16) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              uint32_t b[4];
+              ldsm4(tile_addr<C::TILE>(k_at, kw + 16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)),
+                    b);
+              kf[k][2 * n][0] = b[0], kf[k][2 * n][1] = b[1], kf[k][2 * n + 1][0] = b[2], kf[k][2 * n + 1][1] = b[3];
+            }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t b[4];  // four groups of 8 keys of chunk k
+            ldsm4(tile_addr<C::TILE>(k_at, kw + lane, k), b);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) widen_k(b[n], kf[k][n][0], kf[k][n][1]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        ++it;
+        if (++s == stages) s = 0;
+
+        float col[4][2];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) col[n][0] = col[n][1] = 0.f;
+        const bool tail = j0 + 32 > base;
+        for (int m = 0; m < n16; ++m) {
+          float sc[4][4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t qa[4];
+            ldsm4(q_addr<DT, D>(q_base, m * 16 + (lane & 15), 2 * k + (lane >> 4)), qa);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma<C::F16>(sc[n], qa, kf[k][n][0], kf[k][n][1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rl = m * 16 + (lane >> 2) + 8 * i;
+            const float off = neg_lse[rl];
+            uint32_t vis = off == neg_inf() ? 0u : 0xFFFFFFFFu;  // also keeps 0 x inf of empty rows out
+            if (tail && vis != 0u) {
+              const uint64_t mk = token_mask(a, t0, (c0 + rl) / a.G);
+              vis = seen16(mk, j0, base) | (seen16(mk, j0 + 16, base) << 16);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float x = fast_exp2(fmaf(sc[n][2 * i + e], a.scale_log2, off));
+                col[n][e] += (vis >> (8 * n + 2 * (lane & 3) + e)) & 1u ? x : 0.f;
+              }
+          }
+        }
+        // Sum the eight rows of the warp's lanes; lane q of the first four then holds keys 8n + 2q, + 1.
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) col[n][e] += __shfl_xor_sync(0xFFFFFFFFu, col[n][e], o);
+          }
+        // lane = 4 n' + q writes keys 8 n' + 2 q, + 1 for n' = 0 .. 3
+        float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if ((lane >> 2) == n) w0 = col[n][0], w1 = col[n][1];
+        if (lane < 16) {
+          const int64_t at = (static_cast<int64_t>(p.r) * a.Hkv + g) * a.mass_stride;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int jj = 8 * (lane >> 2) + 2 * (lane & 3) + e, j = j0 + jj;
+            if (j >= keys) continue;
+            // A key of a page that is not there keeps its weight; its status bit is set.
+            const float w = (here >> jj) & 1u ? (e ? w1 : w0) : 0.f;
+            const float old = c0 > 0 ? a.mass_out[at + j] : (j < had ? a.mass_in[at + j] * a.decay : 0.f);
+            a.mass_out[at + j] = old + w;
+          }
+        }
+      }
+    }
+    u += p.t1 - p.t0;
+  }
+  store_status(a, &status_word);
+}
+
+template <int DT, int D>
+cudaError_t run_mass(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
+  using C = Mass<DT, D>;
+  const int stages = C::stages(a.q_rows), smem = C::fixed(a.q_rows) + stages * C::STAGE_BYTES;
+  if (stages < 2) return cudaErrorInvalidValue;
+  const auto kernel = mass_kernel<DT, D>;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::BUDGET);
+  if (e != cudaSuccess) return e;
+  kernel<<<a.groups * a.Hkv, C::THREADS, smem, stream>>>(a, P, stages);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int tree_rows(int max_rows) { return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : 64); }
+int tree_ctas_per_sm(int max_rows) { return tree_rows(max_rows) <= 32 ? 2 : 1; }
+
+cudaError_t launch_tree_attend(int dtype, int D, int max_rows, const DecodeArgs& a, const DecodePlan& P,
+                               cudaStream_t stream) {
+  if (dtype == FP2_BF16 && D == 128) return run_tree_rows<1, 128>(a, P, max_rows, stream);
+  if (dtype == FP2_BF16 && D == 64) return run_tree_rows<1, 64>(a, P, max_rows, stream);
+  if (dtype == FP2_E4M3 && D == 128) return run_tree_rows<2, 128>(a, P, max_rows, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_key_mass(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
+  if (dtype == FP2_BF16 && D == 128) return run_mass<1, 128>(a, P, stream);
+  if (dtype == FP2_BF16 && D == 64) return run_mass<1, 64>(a, P, stream);
+  if (dtype == FP2_E4M3 && D == 128) return run_mass<2, 128>(a, P, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fp2

@@ -15,6 +15,7 @@
 
 #include "../../include/fp2.h"
 #include "fp2_kernels.h"
+#include "serve_kernels.h"
 
 namespace {
 
@@ -515,11 +516,22 @@ cudaError_t ensure_dynamic_smem(const void* kernel, int bytes) {
 
 }  // namespace fp2
 
-// Used by fp2_noalloc.cu only: discovery into a caller-supplied scratch region of a fixed capacity,
+// Used by fp2_serve.cu (errors, hooks, the descriptor encoder) and fp2_noalloc.cu: discovery into a caller-supplied scratch region of a fixed capacity,
 // optionally copying the device status word to status_dev afterwards.
 namespace fp2_internal {
 
 fp2_status set_error(fp2_status s, const char* msg) { return fail(s, msg); }
+
+void clear_error() { g_last_error.clear(); }
+
+void* tensor_map_encoder() { return reinterpret_cast<void*>(get_encode_fn()); }
+
+uint64_t wait_limit_ns() {
+  const int64_t lim = g_wait_limit_ns.load();
+  return lim > 0 ? static_cast<uint64_t>(lim) : 1000000000ull;
+}
+
+int withheld_k_tile() { return static_cast<int>(g_withhold_k_tile.load()); }
 
 fp2_status discover_fixed_scratch(const fp2_problem* problem, const fp2_sparse_params* params,
                                   const fp2_pooled* pooled, const fp2_index* index, void* scratch,
@@ -637,14 +649,28 @@ fp2_status fp2_prefill(const fp2_problem* problem, const fp2_sparse_params* para
 
 fp2_status fp2_get_device_status(const void* scratch, uint32_t* status_out) {
   if (scratch == nullptr || status_out == nullptr) return fail(FP2_ERR_INVALID_ARG, "NULL argument");
-  uint32_t w = 0;
-  const cudaError_t e = cudaMemcpy(&w, scratch, sizeof(w), cudaMemcpyDeviceToHost);
+  uint32_t head[2] = {0, 0};
+  cudaError_t e = cudaMemcpy(head, scratch, sizeof(head), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
+  uint32_t w = head[0];
+  // Decode and eviction calls leave one word per CTA (serve_kernels.h).
+  if ((head[1] & ~fp2::kStatusCount) == fp2::kStatusMagic) {
+    uint32_t words[1024];
+    const uint32_t n = head[1] & fp2::kStatusCount;
+    for (uint32_t i = 0; i < n; i += 1024) {
+      const uint32_t m = std::min<uint32_t>(1024, n - i);
+      e = cudaMemcpy(words, static_cast<const uint32_t*>(scratch) + fp2::kStatusFirst + i, m * sizeof(uint32_t),
+                     cudaMemcpyDeviceToHost);
+      if (e != cudaSuccess) return cuda_fail(e, "status read");
+      for (uint32_t k = 0; k < m; ++k) w |= words[k];
+    }
+  }
   *status_out = w;
   if (w & FP2_DEV_TIMEOUT) return fail(FP2_ERR_TIMEOUT, "a device-side wait timed out");
   if (w & FP2_DEV_CHECK) return fail(FP2_ERR_CHECK_FAILED, "a device-side check of the checked build failed");
-  if (w & (FP2_DEV_PAGE_OOB | FP2_DEV_INDEX_OOB | FP2_DEV_CAPACITY))
-    return fail(FP2_ERR_DEVICE_BOUNDS, "device reported an out-of-range page id, index entry or capacity overflow");
+  if (w & (FP2_DEV_PAGE_OOB | FP2_DEV_INDEX_OOB | FP2_DEV_CAPACITY | FP2_DEV_LEN_OOB | FP2_DEV_SLOT_OOB))
+    return fail(FP2_ERR_DEVICE_BOUNDS,
+                "device reported an out-of-range page id, index entry, length or slot, or a capacity overflow");
   return FP2_OK;
 }
 

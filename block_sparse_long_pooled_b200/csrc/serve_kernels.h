@@ -1,0 +1,131 @@
+// Kernel argument blocks and launchers of the serving operators (internal to the library):
+// rotate.cu, decode.cu, evict.cu; validated and launched by fp2_serve.cu.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/fp2.h"
+
+namespace fp2 {
+
+// Status of the decode and eviction calls.  The prefill clears one word with a memset and its kernels
+// OR into it; at a few microseconds a call, that memset would be a third of a decode step.  Here
+// every CTA keeps its bits in shared memory and stores them to a word of its own when it ends, so
+// nothing has to be cleared: scratch word 0 is zero, word 1 holds kStatusMagic and the number of
+// CTAs, and their words start at byte FP2_SCRATCH_STATUS_BYTES.  fp2_get_device_status reads both
+// forms (the prefill's memset clears word 1).
+constexpr uint32_t kStatusMagic = 0x5E000000u;   // low 24 bits: words that follow
+constexpr uint32_t kStatusCount = 0x00FFFFFFu;
+constexpr int kStatusFirst = 256 / 4;            // FP2_SCRATCH_STATUS_BYTES in words
+
+// ------------------------------------------------------------------ rotate
+
+struct RotateArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* positions;
+  const void* q_norm;  // [d] in the input type, or NULL
+  const void* k_norm;
+  float norm_eps;
+  int Hq, Hkv;         // heads rotated as Q (0: no Q) and as K; Hv heads copied as V
+  int Hv;
+  int rot, interleaved;
+  float rope_scale;
+  void* q_out;
+  void* k_out;
+  void* v_out;
+  int64_t q_out_stride, kv_out_stride;
+  const int64_t* slots;  // NULL: row t
+  int64_t num_slots;
+  float q_inv, k_inv, v_inv;  // 1 / descale (E4M3 output)
+  int64_t tokens;
+  int iters;             // heads per warp / heads per step of a warp
+  uint32_t* status;      // may be NULL
+  uint64_t phase[64];    // turns per position of pair i, as a fraction of 2^64
+};
+
+cudaError_t launch_rotate(int dtype_in, int dtype_out, int D, const RotateArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------------------------ decode
+
+// Query offsets of the batch, passed by value like the prefill's plan.
+struct DecodePlan {
+  int32_t num_seqs;
+  int32_t q_off[FP2_MAX_SEQS + 1];
+};
+
+struct DecodeArgs {
+  CUtensorMap tm_k;  // [page or sequence][token][Hkv][d], box {128 B, 1, rows, 1}
+  CUtensorMap tm_v;
+  const void* q;
+  int64_t q_stride;
+  const int32_t* kv_len;
+  int max_kv_len;
+  const int32_t* page_table;  // NULL: token j of sequence r is row j of outer index r
+  int page_size, max_pages, num_pages;
+  const uint64_t* mask;       // NULL: causal among the drafted tokens
+  int Hq, Hkv, G, T;
+  float scale_log2;           // softmax scale * log2(e) * q_descale * k_descale
+  float v_descale;
+  int groups;                 // CTAs per KV head
+  // tree attention
+  void* out;                  // [T, Hq, d] bf16
+  float* lse;                 // [Hq, T] or NULL
+  int4* desc;                 // [groups] {slot of the first piece of a split item or -1, sequence, row tile, pieces}
+  float2* part_ml;            // [groups * Hkv * 2][rows] running maximum (log2 units) and sum
+  float* part_o;              // [groups * Hkv * 2][rows][d]
+  // key mass
+  const float* lse_in;
+  const float* mass_in;       // NULL: zero
+  float* mass_out;
+  int64_t mass_stride;
+  const int32_t* mass_len;    // keys of each sequence that mass_in holds, or NULL: all
+  float decay;
+  int q_rows;                 // query rows held in shared memory at once
+  uint32_t* scratch;          // status words: see StatusWords
+  uint64_t wait_limit_ns;
+  int withhold;               // testing: the producer skips the load of this local key tile (-1: none)
+};
+
+// Query rows per CTA of the tree attention kernel for at most max_rows rows per (sequence, KV head).
+int tree_rows(int max_rows);
+int tree_ctas_per_sm(int max_rows);
+cudaError_t launch_tree_attend(int dtype, int D, int max_rows, const DecodeArgs& a, const DecodePlan& P,
+                               cudaStream_t stream);
+cudaError_t launch_key_mass(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
+constexpr int kTreeTile = 64;    // keys of a tile of the tree attention kernel
+constexpr int kMassTile = 128;   // keys of a tile of the key mass kernel
+
+// ------------------------------------------------------------------ evict
+
+struct CacheView {
+  char* k;
+  char* v;
+  int64_t stride_tok, stride_outer;  // bytes between tokens, and between pages or sequences
+  const int32_t* page_table;         // NULL: outer index r holds sequence r
+  int rows, max_pages, num_outer;    // tokens per page (or sequence), pages
+};
+
+struct EvictArgs {
+  CacheView src, dst;
+  const int32_t* kv_len;
+  int max_kv_len;
+  int num_seqs, Hkv, row_bytes;  // bytes of one (token, head) row
+  const float* mass;
+  int64_t mass_stride;
+  int budget, sink, window;
+  float* mass_out;               // [num_seqs, Hkv, budget]
+  int32_t* kept;                 // [num_seqs, Hkv, budget]
+  int32_t* kv_len_out;
+  uint32_t* scratch;             // status words: see StatusWords
+};
+
+// CTAs that share one (sequence, KV head): a cluster.
+int evict_cluster(const EvictArgs& a);
+cudaError_t launch_evict(const EvictArgs& a, int cluster, cudaStream_t stream);
+
+}  // namespace fp2

@@ -24,15 +24,18 @@ FP2_OK, FP2_ERR_INVALID_ARG, FP2_ERR_UNSUPPORTED, FP2_ERR_WORKSPACE_TOO_SMALL = 
 FP2_ERR_CUDA, FP2_ERR_DEVICE_BOUNDS, FP2_ERR_TIMEOUT, FP2_ERR_CHECK_FAILED = 4, 5, 6, 7
 FP2_F32, FP2_BF16, FP2_E4M3 = 0, 1, 2
 FP2_DEV_PAGE_OOB, FP2_DEV_INDEX_OOB, FP2_DEV_CAPACITY, FP2_DEV_TIMEOUT, FP2_DEV_CHECK = 0x1, 0x2, 0x4, 0x8, 0x10
+FP2_DEV_LEN_OOB, FP2_DEV_SLOT_OOB = 0x20, 0x40
 FP2_BUILD_CHECKED = 0x1
 FP2_MAX_SEQS, FP2_MAX_BLOCKS = 512, 4096
+FP2_MAX_DRAFT, FP2_MAX_CACHE_LEN = 64, 524288
 
 STATUS_NAMES = {0: "FP2_OK", 1: "FP2_ERR_INVALID_ARG", 2: "FP2_ERR_UNSUPPORTED", 3: "FP2_ERR_WORKSPACE_TOO_SMALL",
                 4: "FP2_ERR_CUDA", 5: "FP2_ERR_DEVICE_BOUNDS", 6: "FP2_ERR_TIMEOUT", 7: "FP2_ERR_CHECK_FAILED"}
 
 EXPORTED = ("fp2_workspace_query", "fp2_workspace_size", "fp2_pool", "fp2_discover", "fp2_attend", "fp2_prefill",
             "fp2_get_device_status", "fp2_last_error", "fp2_version", "fp2_discover_static", "fp2_debug_set",
-            "fp2_build_flags")
+            "fp2_build_flags", "fp2_rotate", "fp2_decode_workspace", "fp2_tree_attend", "fp2_key_mass",
+            "fp2_evict_workspace", "fp2_evict")
 FP2_DEBUG_WAIT_LIMIT_NS, FP2_DEBUG_WITHHOLD_K_TILE, FP2_DEBUG_MISCOUNT_LOAD = 1, 2, 3
 FP2_STATIC_SCRATCH_BYTES = 8 << 20
 
@@ -83,6 +86,59 @@ class fp2_workspace(ctypes.Structure):
     ]
 
 
+class fp2_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("dtype", ctypes.c_int), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("stride_tok", ctypes.c_int64), ("stride_outer", ctypes.c_int64),
+        ("num_outer", ctypes.c_int32), ("rows", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p), ("max_pages_per_seq", ctypes.c_int32),
+    ]
+
+
+class fp2_rotation(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_stride_tok", ctypes.c_int64), ("k_stride_tok", ctypes.c_int64), ("v_stride_tok", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("inv_freq_host", ctypes.POINTER(ctypes.c_double)), ("rope_scale", ctypes.c_float),
+        ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("norm_eps", ctypes.c_float),
+        ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p),
+        ("q_out_stride_tok", ctypes.c_int64), ("kv_out_stride_tok", ctypes.c_int64),
+        ("slots", ctypes.c_void_p), ("num_slots", ctypes.c_int64),
+        ("q_descale", ctypes.c_float), ("k_descale", ctypes.c_float), ("v_descale", ctypes.c_float),
+    ]
+
+
+class fp2_decode(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32),
+        ("cu_seqlens_q_host", ctypes.POINTER(ctypes.c_int32)),
+        ("num_q_heads", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("q_stride_tok", ctypes.c_int64),
+        ("q_descale", ctypes.c_float), ("k_descale", ctypes.c_float), ("v_descale", ctypes.c_float),
+        ("softmax_scale", ctypes.c_float),
+        ("cache", fp2_cache),
+        ("kv_len", ctypes.c_void_p), ("max_kv_len", ctypes.c_int32),
+        ("tree_mask", ctypes.c_void_p),
+    ]
+
+
+class fp2_eviction(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32),
+        ("src", fp2_cache), ("dst", fp2_cache),
+        ("kv_len", ctypes.c_void_p), ("max_kv_len", ctypes.c_int32),
+        ("mass", ctypes.c_void_p), ("mass_stride", ctypes.c_int64),
+        ("budget", ctypes.c_int32), ("sink", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("mass_out", ctypes.c_void_p), ("kept", ctypes.c_void_p), ("kv_len_out", ctypes.c_void_p),
+    ]
+
+
 class FP2Error(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -110,8 +166,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp2_prefill.argtypes = [P(fp2_problem), P(fp2_sparse_params), vp, vp, vp, sz, vp]
     lib.fp2_get_device_status.argtypes = [vp, P(ctypes.c_uint32)]
     lib.fp2_discover_static.argtypes = [P(fp2_problem), P(fp2_sparse_params), P(fp2_pooled), P(fp2_index), vp, vp]
+    lib.fp2_rotate.argtypes = [P(fp2_rotation), vp, vp]
+    lib.fp2_decode_workspace.argtypes = [P(fp2_decode), P(sz)]
+    lib.fp2_tree_attend.argtypes = [P(fp2_decode), vp, vp, vp, sz, vp]
+    lib.fp2_key_mass.argtypes = [P(fp2_decode), vp, vp, vp, ctypes.c_int64, vp, ctypes.c_float, vp, sz, vp]
+    lib.fp2_evict_workspace.argtypes = [P(fp2_eviction), P(sz)]
+    lib.fp2_evict.argtypes = [P(fp2_eviction), vp, sz, vp]
     for name in ("fp2_workspace_query", "fp2_workspace_size", "fp2_pool", "fp2_discover", "fp2_attend", "fp2_prefill",
-                 "fp2_get_device_status", "fp2_discover_static"):
+                 "fp2_get_device_status", "fp2_discover_static", "fp2_rotate", "fp2_decode_workspace",
+                 "fp2_tree_attend", "fp2_key_mass", "fp2_evict_workspace", "fp2_evict"):
         getattr(lib, name).restype = ctypes.c_int
     lib.fp2_debug_set.argtypes = [ctypes.c_int32, ctypes.c_int64]
     lib.fp2_debug_set.restype = ctypes.c_int
@@ -323,3 +386,335 @@ def alloc_scratch(nbytes: int, device):
 def out_dtype(problem: Problem):
     import torch
     return torch.float32 if problem.struct.dtype == FP2_F32 else torch.bfloat16
+
+
+# ------------------------------------------------------------------ serving: positions, decode, eviction
+
+@dataclasses.dataclass
+class Rope:
+    """Frequencies of a rotary embedding: pair i turns by position * inv_freq[i] radians."""
+    inv_freq: np.ndarray            # float64 [rotary_dim / 2]
+    interleaved: bool = False       # pairs (2i, 2i+1); else (i, i + rotary_dim/2)
+    scale: float = 1.0              # factor on cosine and sine
+
+
+def make_rope(inv_freq, interleaved: bool = False, scale: float = 1.0) -> Rope:
+    """inv_freq: host sequence or array; its length is half the rotary dimension (a multiple of 8)."""
+    f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+    if f.ndim != 1:
+        raise ValueError("inv_freq must be one-dimensional")
+    return Rope(f, bool(interleaved), float(scale))
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                     original_len: int = 8192, low: float = 1.0, high: float = 4.0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0) -> tuple:
+    """(inverse frequencies, factor on cosine and sine) for make_rope.
+
+    scaling None: base^(-2i/rotary_dim).  "linear": divided by factor.  "ntk": the base is raised so
+    that the slowest pair is slowed down by factor.  "llama3": pairs that turn less than `low` times in
+    original_len are divided by factor, those above `high` times kept, linear in the turns between.
+    "yarn": kept above beta_fast turns, divided below beta_slow, linear in the pair's index between,
+    and cosine and sine scaled by 0.1 ln(factor) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be a positive even number")
+    if not factor > 0 or not base > 1:
+        raise ValueError("factor must be positive and base above 1")
+    if scaling == "ntk":
+        base = base * factor ** (rotary_dim / max(rotary_dim - 2, 1))
+    f = base ** (-np.arange(0, rotary_dim, 2, dtype=np.float64) / rotary_dim)
+    if scaling in (None, "none", "ntk"):
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "llama3":
+        t = np.clip((original_len * f / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
+        return f * ((1 - t) / factor + t), 1.0
+    if scaling == "yarn":
+        def pair(turns):   # index of the pair that turns that often in original_len
+            return rotary_dim * np.log(original_len / (turns * 2 * np.pi)) / (2 * np.log(base))
+        first, last = max(np.floor(pair(beta_fast)), 0), min(np.ceil(pair(beta_slow)), rotary_dim - 1)
+        t = np.clip((np.arange(rotary_dim // 2) - first) / max(last - first, 0.001), 0.0, 1.0)
+        return f * (1 - t + t / factor), float(0.1 * np.log(factor) + 1.0) if factor > 1 else 1.0
+    raise ValueError(f"unknown scaling {scaling!r}")
+
+
+class _Handle:
+    """A C struct, the tensors it points into (kept alive here) and the device they are on."""
+
+    def __init__(self, struct, tensors, arrays=()):
+        self.struct, self.ref = struct, ctypes.byref(struct)
+        self.keep = (tuple(tensors), tuple(arrays))
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) > 1:
+            raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+        device = devices.pop()
+        self.device = device
+        self.index = device.index if device.type == "cuda" else None
+
+    def call(self, name: str, *args, stream=None):
+        """The C entry point on this handle, on its device and (stream None) that device's current stream."""
+        import torch
+        fn = getattr(load_library(), name)
+        if self.index is None:
+            return _check(fn(self.ref, *args, 0 if stream is None else _stream_handle(stream)))
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(self.index)   # current_stream(...).cuda_stream, without the object
+        else:
+            raw = _stream_handle(stream)
+        if torch._C._cuda_getDevice() == self.index:
+            return _check(fn(self.ref, *args, raw))
+        with torch.cuda.device(self.index):
+            return _check(fn(self.ref, *args, raw))
+
+    def pointer(self, t, dtype, shape, what: str):
+        """data_ptr of a contiguous tensor of this handle's device, or None."""
+        if t is None:
+            return None
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}")
+        return t.data_ptr()
+
+
+class Rotation(_Handle):
+    pass
+
+
+class Decode(_Handle):
+    pass
+
+
+class Eviction(_Handle):
+    pass
+
+
+@dataclasses.dataclass
+class Cache:
+    """An fp2_cache and the tensors it points into."""
+    struct: fp2_cache
+    keep: tuple
+
+
+def _head_rows(t, what: str, dims: int = 3):
+    """Check that the last two dimensions of t, [..., heads, d], are dense."""
+    if t.dim() != dims:
+        raise ValueError(f"{what} must have {dims} dimensions")
+    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
+        raise ValueError(f"heads of {what} must be dense (strides (d, 1))")
+
+
+def _expect(t, dtype, shape, what: str):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _stored_like(a, b) -> bool:
+    return _dtype_code(a) == _dtype_code(b)
+
+
+def make_cache(k, v=None, page_table=None) -> Cache:
+    """k, v: [num_pages, page_size, Hkv, d] with page_table [num_seqs, max_pages] (int32), or without one
+    [num_seqs, rows, Hkv, d].  v may be None for fp2_key_mass."""
+    import torch
+    _head_rows(k, "k", 4)
+    if v is not None:
+        _head_rows(v, "v", 4)
+        if tuple(v.shape) != tuple(k.shape) or not _stored_like(k, v) or v.device != k.device:
+            raise ValueError("k and v must agree in shape, dtype and device")
+        if any(v.shape[i] > 1 and v.stride(i) != k.stride(i) for i in (0, 1)):
+            raise ValueError("k and v must have the same strides")
+    c = fp2_cache()
+    c.k, c.v, c.dtype = _ptr(k), _ptr(v), _dtype_code(k)
+    c.num_outer, c.rows, c.num_kv_heads, c.head_dim = k.shape
+    hd = k.shape[2] * k.shape[3]
+    c.stride_tok = k.stride(1) if k.shape[1] > 1 else hd
+    c.stride_outer = k.stride(0) if k.shape[0] > 1 else c.rows * c.stride_tok
+    if page_table is not None:
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+            raise ValueError("page_table must be a contiguous int32 tensor [num_seqs, max_pages]")
+        if page_table.device != k.device:
+            raise ValueError("page_table must be on the cache's device")
+        c.page_table, c.max_pages_per_seq = _ptr(page_table), page_table.shape[1]
+    return Cache(c, (k, v, page_table))
+
+
+def _check_table(cache: Cache, num_seqs: int):
+    table = cache.keep[2]
+    if table is not None and table.shape[0] < num_seqs:
+        raise ValueError("page_table has fewer rows than there are sequences")
+
+
+def make_rotate(q, k, v, positions, rope: Optional[Rope], q_out, k_out, v_out, slots=None, q_norm=None, k_norm=None,
+                norm_eps: float = 1e-6, q_descale: float = 1.0, k_descale: float = 1.0,
+                v_descale: float = 1.0) -> Rotation:
+    """q [T, Hq, d], k and v [T, Hkv, d] (views of one projection's output will do; q, or k and v, or v
+    alone may be None); positions [T] int32; rope from make_rope, or None (norms and copies only).
+    q_out [T, Hq, d]; k_out, v_out [rows, Hkv, d] or a paged cache [pages, page_size, Hkv, d], whose
+    row slots[t] (int64, < 0: none) token t's K and V go to; without slots, row t."""
+    import torch
+    given = [(x, n) for x, n in ((q, "q"), (k, "k"), (v, "v")) if x is not None]
+    if not given or (k is None and v is not None):
+        raise ValueError("q or k must be given, and v only with k")
+    first = given[0][0]
+    T, d = first.shape[0], first.shape[-1]
+    for x, n in given:
+        _head_rows(x, n)
+        if x.shape[0] != T or x.shape[2] != d or x.dtype != first.dtype:
+            raise ValueError("q, k and v must agree in tokens, head_dim and dtype")
+    if v is not None and v.shape[1] != k.shape[1]:
+        raise ValueError("k and v must have the same heads")
+    s = fp2_rotation()
+    s.tokens, s.head_dim, s.in_dtype = T, d, _dtype_code(first)
+    outs = [(q, q_out, "q_out"), (k, k_out, "k_out"), (v, v_out, "v_out")]
+    outs = [(x, o, n) for x, o, n in outs if x is not None]
+    if any(o is None for _, o, _ in outs):
+        raise ValueError("every input needs its output")
+    s.out_dtype = _dtype_code(outs[0][1])
+    if any(_dtype_code(o) != s.out_dtype for _, o, _ in outs):
+        raise ValueError("outputs must have one dtype")
+
+    def stride(x):
+        return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+    if q is not None:
+        _head_rows(q_out, "q_out")
+        if tuple(q_out.shape) != tuple(q.shape):
+            raise ValueError("q_out must have q's shape")
+        s.num_q_heads, s.q, s.q_stride_tok = q.shape[1], _ptr(q), stride(q)
+        s.q_out, s.q_out_stride_tok = _ptr(q_out), stride(q_out)
+    if k is not None:
+        rows, steps = None, []
+        for x, o, n in outs:
+            if x is q:
+                continue
+            _head_rows(o, n, o.dim())
+            if o.dim() not in (3, 4) or tuple(o.shape[-2:]) != tuple(x.shape[1:]):
+                raise ValueError(f"{n} must be [rows, Hkv, d] or [pages, page_size, Hkv, d]")
+            step = o.stride(-3) if o.shape[-3] > 1 else (o.stride(0) if o.dim() == 4 else o.shape[-2] * o.shape[-1])
+            if o.dim() == 4 and o.shape[0] > 1 and o.stride(0) != o.shape[1] * step:
+                raise ValueError(f"pages of {n} must follow each other without a gap")
+            steps.append(step)
+            rows = o.shape[0] if o.dim() == 3 else o.shape[0] * o.shape[1]
+            s.num_slots = rows if not s.num_slots else min(rows, s.num_slots)
+        if len(set(steps)) != 1:
+            raise ValueError("k_out and v_out must have the same token stride")
+        s.num_kv_heads, s.k, s.k_stride_tok, s.k_out = k.shape[1], _ptr(k), stride(k), _ptr(k_out)
+        s.kv_out_stride_tok = max(steps[0], k.shape[1] * d)
+        if v is not None:
+            s.v, s.v_stride_tok, s.v_out = _ptr(v), stride(v), _ptr(v_out)
+    arrays = ()
+    if rope is not None:
+        arrays = (rope.inv_freq,)
+        s.rotary_dim, s.interleaved, s.rope_scale = 2 * len(rope.inv_freq), int(rope.interleaved), rope.scale
+        s.inv_freq_host = rope.inv_freq.ctypes.data_as(ctypes.POINTER(ctypes.c_double))
+        _expect(positions, torch.int32, (T,), "positions")
+        s.positions = _ptr(positions)
+    _expect(slots, torch.int64, (T,), "slots")
+    _expect(q_norm, first.dtype, (d,), "q_norm")
+    _expect(k_norm, first.dtype, (d,), "k_norm")
+    s.slots, s.q_norm, s.k_norm, s.norm_eps = _ptr(slots), _ptr(q_norm), _ptr(k_norm), norm_eps
+    s.q_descale, s.k_descale, s.v_descale = q_descale, k_descale, v_descale
+    return Rotation(s, (q, k, v, positions if rope is not None else None, slots, q_norm, k_norm, q_out, k_out, v_out),
+                    arrays)
+
+
+def fp2_rotate(rotation: Rotation, status_dev=None, stream=None):
+    """Head norms, rotary positions and cache append (include/fp2.h).  status_dev: optional int32/uint32
+    device word that FP2_DEV_* bits are OR-ed into."""
+    rotation.call("fp2_rotate", _ptr(status_dev), stream=stream)
+
+
+def make_decode(q, cache: Cache, cu_seqlens, kv_len, max_kv_len: int, num_kv_heads: Optional[int] = None,
+                tree_mask=None, q_descale: float = 1.0, k_descale: float = 1.0, v_descale: float = 1.0,
+                softmax_scale: float = 0.0) -> Decode:
+    """q [T, Hq, d]: the new tokens of each sequence, cu_seqlens (host, [num_seqs + 1]) their offsets.
+    kv_len [num_seqs] int32 on the device: keys per sequence, the new ones (already in the cache)
+    included; max_kv_len: a bound on them.  tree_mask [T] int64 (bit b: the token sees new key b), or
+    None: a chain."""
+    import torch
+    _head_rows(q, "q")
+    c = cache.struct
+    if num_kv_heads is not None and num_kv_heads != c.num_kv_heads:
+        raise ValueError("num_kv_heads differs from the cache's")
+    if q.shape[2] != c.head_dim or _dtype_code(q) != c.dtype:
+        raise ValueError("q must have the cache's head_dim and dtype")
+    cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+    if cu.ndim != 1 or len(cu) < 2 or cu[-1] != q.shape[0]:
+        raise ValueError("cu_seqlens must end at the number of tokens of q")
+    _check_table(cache, len(cu) - 1)
+    _expect(kv_len, torch.int32, (len(cu) - 1,), "kv_len")
+    _expect(tree_mask, torch.int64, (q.shape[0],), "tree_mask")
+    s = fp2_decode()
+    s.num_seqs, s.cu_seqlens_q_host = len(cu) - 1, cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    s.num_q_heads, s.q = q.shape[1], _ptr(q)
+    s.q_stride_tok = q.stride(0) if q.shape[0] > 1 else q.shape[1] * q.shape[2]
+    s.q_descale, s.k_descale, s.v_descale, s.softmax_scale = q_descale, k_descale, v_descale, softmax_scale
+    s.cache = c
+    s.kv_len, s.max_kv_len, s.tree_mask = _ptr(kv_len), max_kv_len, _ptr(tree_mask)
+    return Decode(s, (q, kv_len, tree_mask, *cache.keep), (cu,))
+
+
+def fp2_decode_workspace(decode: Decode) -> int:
+    """Scratch bytes of fp2_tree_attend and fp2_key_mass."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().fp2_decode_workspace(decode.ref, ctypes.byref(n)))
+    return n.value
+
+
+def fp2_tree_attend(decode: Decode, out, lse, scratch, stream=None):
+    """Attention of the new tokens over their caches.  out [T, Hq, d] bf16; lse [Hq, T] f32 or None."""
+    import torch
+    s = decode.struct
+    T, hq, d = decode.keep[0][0].shape
+    if s.cache.v is None:
+        raise ValueError("the cache has no v")
+    decode.call("fp2_tree_attend", decode.pointer(out, torch.bfloat16, (T, hq, d), "out"),
+                decode.pointer(lse, torch.float32, (hq, T), "lse"), scratch.data_ptr(), scratch.nbytes, stream=stream)
+
+
+def fp2_key_mass(decode: Decode, lse, mass_in, mass_out, scratch, decay: float = 1.0, mass_len=None, stream=None):
+    """mass_out = decay * mass_in + the attention weight that each key receives from the new tokens.
+    lse [Hq, T] from fp2_tree_attend; mass_in (or None: zero), mass_out [num_seqs, Hkv, >= max_kv_len]
+    f32 (they may be one tensor); mass_len [num_seqs] int32: keys that mass_in covers, or None: all."""
+    import torch
+    s = decode.struct
+    shape = (s.num_seqs, s.cache.num_kv_heads, mass_out.shape[-1])
+    T, hq, _ = decode.keep[0][0].shape
+    decode.call("fp2_key_mass", decode.pointer(lse, torch.float32, (hq, T), "lse"),
+                decode.pointer(mass_in, torch.float32, shape, "mass_in"),
+                decode.pointer(mass_out, torch.float32, shape, "mass_out"), shape[2],
+                decode.pointer(mass_len, torch.int32, (s.num_seqs,), "mass_len"), decay, scratch.data_ptr(),
+                scratch.nbytes, stream=stream)
+
+
+def make_evict(cache: Cache, kv_len, max_kv_len: int, mass, budget: int, sink: int, window: int, cache_out: Cache,
+               mass_out, kept, kv_len_out) -> Eviction:
+    """cache, kv_len [num_seqs] int32, mass [num_seqs, Hkv, >= max_kv_len] f32: the keys and their weights.
+    cache_out gets the kept rows; mass_out [num_seqs, Hkv, budget] f32 and kept (int32, the same shape)
+    their weights and old indexes, kv_len_out [num_seqs] int32 the new lengths."""
+    import torch
+    n, c = kv_len.shape[0], cache.struct
+    _check_table(cache, n)
+    _check_table(cache_out, n)
+    _expect(kv_len, torch.int32, (n,), "kv_len")
+    _expect(mass, torch.float32, (n, c.num_kv_heads, mass.shape[-1]), "mass")
+    _expect(mass_out, torch.float32, (n, c.num_kv_heads, budget), "mass_out")
+    _expect(kept, torch.int32, (n, c.num_kv_heads, budget), "kept")
+    _expect(kv_len_out, torch.int32, (n,), "kv_len_out")
+    s = fp2_eviction()
+    s.num_seqs, s.src, s.dst = n, c, cache_out.struct
+    s.kv_len, s.max_kv_len, s.mass, s.mass_stride = _ptr(kv_len), max_kv_len, _ptr(mass), mass.shape[-1]
+    s.budget, s.sink, s.window = budget, sink, window
+    s.mass_out, s.kept, s.kv_len_out = _ptr(mass_out), _ptr(kept), _ptr(kv_len_out)
+    return Eviction(s, (kv_len, mass, mass_out, kept, kv_len_out, *cache.keep, *cache_out.keep))
+
+
+def fp2_evict_workspace(eviction: Eviction) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().fp2_evict_workspace(eviction.ref, ctypes.byref(n)))
+    return n.value
+
+
+def fp2_evict(eviction: Eviction, scratch, stream=None):
+    """Keep each (sequence, KV head)'s heaviest keys, in another cache (include/fp2.h)."""
+    eviction.call("fp2_evict", scratch.data_ptr(), scratch.nbytes, stream=stream)

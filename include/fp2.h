@@ -72,6 +72,8 @@ extern "C" {
 
 #define FP2_MAX_SEQS 512
 #define FP2_MAX_BLOCKS 4096
+#define FP2_MAX_DRAFT 64          /* query tokens per sequence of a decode call */
+#define FP2_MAX_CACHE_LEN 524288  /* keys per sequence of a decode or eviction call */
 
 typedef enum {
   FP2_OK = 0,
@@ -91,6 +93,8 @@ typedef enum { FP2_F32 = 0, FP2_BF16 = 1, FP2_E4M3 = 2 } fp2_dtype;
 #define FP2_DEV_INDEX_OOB 0x2u     /* CSR column outside [0, i] / not ascending / diagonal missing */
 #define FP2_DEV_CAPACITY 0x4u      /* kept blocks exceed fp2_index.col_capacity */
 #define FP2_DEV_TIMEOUT 0x8u       /* an mbarrier wait gave up */
+#define FP2_DEV_LEN_OOB 0x20u      /* decode, eviction: a kv_len outside [drafted tokens, max_kv_len] */
+#define FP2_DEV_SLOT_OOB 0x40u     /* rotate: a slot >= num_slots; that token's K and V were not written */
 #define FP2_DEV_CHECK 0x10u        /* checked build only: a hand-off count or an index bound did not
                                       hold where it was checked; the guarded access was skipped */
 
@@ -231,6 +235,130 @@ FP2_API fp2_status fp2_prefill(const fp2_problem* problem, const fp2_sparse_para
  * the stream has been synchronised).  *status_out gets the raw FP2_DEV_* bits; the
  * return value maps them to FP2_ERR_DEVICE_BOUNDS / FP2_ERR_TIMEOUT, else FP2_OK. */
 FP2_API fp2_status fp2_get_device_status(const void* scratch, uint32_t* status_out);
+
+/* ------------------------------------------------------------------ serving
+ *
+ * The operators around the prefill that a serving loop needs on the same cache: positions and cache
+ * append before it, attention of the tokens that follow, and eviction when the cache outgrows its
+ * budget.  Same conventions as above; in addition
+ *   - lengths of the cache live on the device (kv_len), so a captured decode step can be replayed
+ *     while the cache grows; the host gives their upper bound max_kv_len.  A length outside
+ *     [q_len, max_kv_len] sets FP2_DEV_LEN_OOB and the sequence counts as empty;
+ *   - scratch belongs to one call at a time: calls that may overlap on the GPU (streams, graphs) take
+ *     separate scratch.  The status word of these calls is read the same way, by
+ *     fp2_get_device_status on the call's scratch.
+ */
+
+/* A KV cache: K and V are [num_outer, rows, Hkv, d].  With a page table, outer indexes are pages of
+ * `rows` tokens and token j of sequence r is row j % rows of page page_table[r][j / rows]; without
+ * one, outer index r holds sequence r.  Both have the same strides. */
+typedef struct {
+  void* k;
+  void* v;
+  fp2_dtype dtype;
+  int32_t num_kv_heads, head_dim;
+  int64_t stride_tok;                /* elements between tokens (>= Hkv*d) */
+  int64_t stride_outer;              /* elements between pages or sequences (>= rows*stride_tok) */
+  int32_t num_outer, rows;           /* pages or sequences; tokens in each (paged: a power of two >= 16) */
+  const int32_t* page_table;         /* device [num_seqs, max_pages_per_seq] or NULL */
+  int32_t max_pages_per_seq;
+} fp2_cache;
+
+/* Head norms, rotary positions and cache append of one projection's output. */
+typedef struct {
+  int64_t tokens;
+  int32_t num_q_heads, num_kv_heads; /* 0: no Q, or no K and V; V may also be left out alone (v NULL) */
+  int32_t head_dim;                  /* 64 or 128 */
+  fp2_dtype in_dtype;                /* FP2_BF16 or FP2_F32: q, k, v and the norm weights */
+  fp2_dtype out_dtype;               /* in_dtype, or FP2_E4M3 */
+  const void* q;                     /* device, [tokens, heads, d] with a token stride (elements) each */
+  const void* k;
+  const void* v;
+  int64_t q_stride_tok, k_stride_tok, v_stride_tok;
+  const int32_t* positions;          /* device [tokens]; NULL when rotary_dim is 0 */
+  int32_t rotary_dim;                /* leading values of a head that turn: a multiple of 16, <= d; 0: none */
+  int32_t interleaved;               /* pairs (2i, 2i+1); else (i, i + rotary_dim/2) */
+  const double* inv_freq_host;       /* HOST [rotary_dim/2]: pair i turns by position * inv_freq[i] radians */
+  float rope_scale;                  /* factor on cosine and sine (YaRN's attention factor); 0 -> 1 */
+  const void* q_norm;                /* device [d] in in_dtype, or NULL: x * q_norm / sqrt(mean(x^2) + eps) */
+  const void* k_norm;
+  float norm_eps;
+  void* q_out;                       /* device, [tokens, Hq, d] */
+  void* k_out;                       /* device, rows of [Hkv, d]: row slots[t], or row t without slots */
+  void* v_out;
+  int64_t q_out_stride_tok, kv_out_stride_tok;
+  const int64_t* slots;              /* device [tokens] or NULL; < 0: K and V of that token are not written */
+  int64_t num_slots;                 /* rows of k_out and v_out */
+  float q_descale, k_descale, v_descale;  /* E4M3 output: stored = value / descale; else 1 */
+} fp2_rotation;
+
+/* Rotate: x' = norm(x) per head, pairs of the first rotary_dim values turn by their angle, V passes
+ * through; one rounding, to out_dtype (E4M3 saturates at 448).  Angles are exact at any int32
+ * position (no fp32 product of position and frequency).  An output may be its own input (same
+ * pointer, stride and type; without slots); otherwise outputs must not overlap inputs.  Slots that
+ * are >= 0 must be distinct.  status_dev: device word that FP2_DEV_* bits are OR-ed into, or NULL;
+ * not cleared.  No scratch. */
+FP2_API fp2_status fp2_rotate(const fp2_rotation* rotation, uint32_t* status_dev, fp2_stream_t stream);
+
+/* Queries of a decode step: q_len(r) <= FP2_MAX_DRAFT tokens at the end of each sequence, whose K
+ * and V are the last q_len(r) of the kv_len[r] keys in the cache. */
+typedef struct {
+  int32_t num_seqs;
+  const int32_t* cu_seqlens_q_host;  /* HOST [num_seqs+1]; a sequence may have no tokens */
+  int32_t num_q_heads;
+  const void* q;                     /* device [T, Hq, d] in the cache's dtype */
+  int64_t q_stride_tok;
+  float q_descale, k_descale, v_descale;  /* value = stored * descale; 1.0 unless E4M3 */
+  float softmax_scale;               /* 0 -> 1/sqrt(head_dim) */
+  fp2_cache cache;                   /* FP2_BF16, or FP2_E4M3 with head_dim 128 */
+  const int32_t* kv_len;             /* device [num_seqs]: keys per sequence, drafted ones included */
+  int32_t max_kv_len;                /* no kv_len is above it; <= FP2_MAX_CACHE_LEN */
+  const uint64_t* tree_mask;         /* device [T] or NULL.  Bit b of a token's word: it sees drafted key b
+                                        (its own included only if its bit is set).  NULL: a chain, token i
+                                        sees drafted keys 0 .. i.  Every token sees all earlier keys. */
+} fp2_decode;
+
+/* Scratch bytes of fp2_tree_attend and fp2_key_mass.  Host only; launches nothing. */
+FP2_API fp2_status fp2_decode_workspace(const fp2_decode* decode, size_t* scratch_bytes);
+
+/* Tree attention (one token per sequence: a plain decode step).
+ * out: [T, Hq, d] bf16, 16-byte aligned; lse: [Hq, T] f32 natural-log normaliser, or NULL.  A token
+ * that sees no key gets zeros and -infinity.  Keys that a token does not see have no influence on
+ * it, whatever their values (NaN included). */
+FP2_API fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void* scratch,
+                                   size_t scratch_bytes, fp2_stream_t stream);
+
+/* The attention weight that each key receives from the call's tokens, summed over them and over the
+ * heads of its group, added to a decayed earlier sum:
+ *   mass_out[r][g][j] = decay * mass_in[r][g][j] + sum_{h of g, t sees j} exp(q_t,h . k_j scale - lse[h][t])
+ * mass: [num_seqs, Hkv, mass_stride] f32, mass_stride >= max_kv_len; mass_in may be NULL (zero) or
+ * mass_out itself.  mass_len: device [num_seqs], how many keys mass_in covers (later ones count as
+ * zero), or NULL: kv_len.  lse as fp2_tree_attend writes it.  Entries from kv_len on are left alone.
+ * V is not read (cache.v may be NULL). */
+FP2_API fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, const float* mass_in, float* mass_out,
+                                int64_t mass_stride, const int32_t* mass_len, float decay, void* scratch,
+                                size_t scratch_bytes, fp2_stream_t stream);
+
+/* Eviction by accumulated weight.  Per (sequence r, KV head g), N = min(kv_len[r], budget) keys stay:
+ * all when they fit, else the first `sink`, the last `window` and the heaviest of the others (ties:
+ * lowest index; NaN counts as heaviest).  They are written to rows 0 .. N-1 of dst in ascending order. */
+typedef struct {
+  int32_t num_seqs;
+  fp2_cache src, dst;                /* same dtype (any, head_dim 64 or 128), heads and head_dim; no overlap */
+  const int32_t* kv_len;             /* device [num_seqs] */
+  int32_t max_kv_len;                /* <= FP2_MAX_CACHE_LEN */
+  const float* mass;                 /* device [num_seqs, Hkv, mass_stride] */
+  int64_t mass_stride;               /* >= max_kv_len */
+  int32_t budget, sink, window;      /* budget >= 1, sink + window <= budget */
+  float* mass_out;                   /* device [num_seqs, Hkv, budget]: weights of the kept keys, then 0 */
+  int32_t* kept;                     /* device [num_seqs, Hkv, budget]: their old indexes, then -1 */
+  int32_t* kv_len_out;               /* device [num_seqs]: N */
+} fp2_eviction;
+
+FP2_API fp2_status fp2_evict_workspace(const fp2_eviction* eviction, size_t* scratch_bytes);
+/* Rows of dst from N on are left alone.  A row whose source or destination page id is out of range
+ * is not written (FP2_DEV_PAGE_OOB); kept and mass_out are. */
+FP2_API fp2_status fp2_evict(const fp2_eviction* eviction, void* scratch, size_t scratch_bytes, fp2_stream_t stream);
 
 /* Size of the device buffer fp2_discover_static uses in place of caller scratch. */
 #define FP2_STATIC_SCRATCH_BYTES (8u << 20)
