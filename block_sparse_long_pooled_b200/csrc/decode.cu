@@ -9,29 +9,16 @@
 // head; kv_len lives on the device, so each CTA scans it and takes an equal share of that axis.  A
 // grid of `groups` x KV heads puts the KV heads of one share side by side in time: their rows are
 // neighbours in DRAM.  An (item = sequence, row tile) that several groups share leaves partial
-// results in scratch, and combine_kernel joins them in group order, so results do not depend on
+// results in scratch, and join_kernel joins them in group order, so results do not depend on
 // timing.  One producer warp brings K/V tiles in by TMA (page by page), consumer warps run
 // mma.sync on them: a tile has 16 to 64 query rows, below the 128 of a tcgen05 tile, and the legacy
 // tensor path keeps pace with HBM up to there.
-#include "fp2_device.cuh"
-#include "fp2_kernels.h"
-#include "serve_kernels.h"
+#include "decode_device.cuh"
 
 namespace fp2 {
 
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-
-// ------------------------------------------------------------------ small PTX wrappers
-
-FP2_DEVICE void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
 FP2_DEVICE void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -60,71 +47,9 @@ template <int N>
 FP2_DEVICE void consumer_sync() {  // the N consumer threads only (barrier 1)
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
-FP2_DEVICE float neg_inf() { return __uint_as_float(0xFF800000u); }
-FP2_DEVICE float pos_inf() { return __uint_as_float(0x7F800000u); }
-
-// ------------------------------------------------------------------ the axis of units
-
-// Keys of sequence r, or -1 when its length is no valid one (below its drafted tokens, above
-// max_kv_len): such a sequence has one empty tile and its rows see nothing.
-FP2_DEVICE int seq_keys(const DecodeArgs& a, const DecodePlan& P, int r) {
-  const int n = a.kv_len[r];
-  return (n < P.q_off[r + 1] - P.q_off[r] || n > a.max_kv_len) ? -1 : n;
-}
-
-// Lengths into len[] and the exclusive prefix of the units per sequence into pre[0 .. num_seqs]:
-// units = row tiles (at least least_tiles) * max(1, key tiles).  The whole block reads the lengths at once (one trip to
-// memory whatever the batch), one warp adds up.  Ends with the block synchronised.
-template <int TILE>
-FP2_DEVICE void scan_units(const DecodeArgs& a, const DecodePlan& P, int rows_per_tile, int least_tiles, long long* pre,
-                           int* len, uint32_t* status) {
-  for (int r = threadIdx.x; r < P.num_seqs; r += blockDim.x) {
-    len[r] = seq_keys(a, P, r);
-    if (len[r] < 0) set_status(status, FP2_DEV_LEN_OOB);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    long long run = 0;
-    for (int base = 0; base < P.num_seqs; base += 32) {
-      const int r = base + lane;
-      long long u = 0;
-      if (r < P.num_seqs) {
-        const int rows = (P.q_off[r + 1] - P.q_off[r]) * a.G;
-        const int tiles = len[r] <= 0 ? 1 : (len[r] + TILE - 1) / TILE;
-        u = static_cast<long long>(max((rows + rows_per_tile - 1) / rows_per_tile, least_tiles)) * tiles;
-      }
-      long long inc = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (r < P.num_seqs) pre[r] = run + inc - u;
-      run += __shfl_sync(0xFFFFFFFFu, inc, 31);
-    }
-    if (lane == 0) pre[P.num_seqs] = run;
-  }
-  __syncthreads();
-}
-
-// The CTA's status bits go to a word of its own in scratch (see serve_kernels.h); every thread
-// calls it, with nothing of the CTA's left to do.
-FP2_DEVICE void store_status(const DecodeArgs& a, const uint32_t* status) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    a.scratch[kStatusFirst + blockIdx.x] = *status;
-    if (blockIdx.x == 0) *reinterpret_cast<uint2*>(a.scratch) = make_uint2(0u, kStatusMagic | gridDim.x);
-  }
-}
-
 struct Piece {  // key tiles [t0, t1) of one item
   int r, rt, t0, t1, tiles;
 };
-
-FP2_DEVICE int active_groups(long long units, int groups) {
-  return static_cast<int>(units < 1 ? 1 : (units < groups ? units : groups));
-}
 
 // The piece that starts at unit u (u < u1 <= pre[num_seqs]).
 template <int TILE>
@@ -144,76 +69,6 @@ FP2_DEVICE Piece piece_at(const long long* pre, const int* len, int num_seqs, lo
   p.t1 = p.tiles - p.t0 <= left ? p.tiles : p.t0 + static_cast<int>(left);
   return p;
 }
-
-// ------------------------------------------------------------------ producer
-
-// One tile (TILE keys from key j0) of K, and of V when v_off is given, into a stage: page by page,
-// boxes of 128 bytes x up to 64 rows.  Called by a whole warp; the page ids of 32 pages at a time
-// sit in the lanes.  Returns through *valid (64 bits a word) which rows hold a key of the sequence:
-// rows past its end and rows of a page id out of range do not.
-template <int TILE, int ELT, int D>
-struct Producer {
-  static constexpr int HALVES = D * ELT / 128;            // boxes side by side
-  int page_base = -1, page_id = -1, seq = -1;             // lanes hold pages page_base .. + 31 of sequence seq
-
-  FP2_DEVICE void load(const DecodeArgs& a, const Piece& p, int keys, int g, int j0, uint32_t k_smem, uint32_t v_smem,
-                       uint64_t* bar, uint64_t* valid, uint32_t* status, bool withhold) {
-    const int lane = threadIdx.x & 31;
-    const bool paged = a.page_table != nullptr;
-    const int step = paged && a.page_size < 64 ? a.page_size : 64;
-    const int end = keys < j0 + TILE ? keys : j0 + TILE;
-    uint64_t ok[TILE / 64];
-#pragma unroll
-    for (int w = 0; w < TILE / 64; ++w) ok[w] = 0;
-    uint32_t bytes = 0;
-    // First the boxes are counted, then the barrier is armed, then they are issued.
-    for (int pass = 0; pass < 2; ++pass) {
-      for (int j = j0; j < end; j += step) {
-        int outer = p.r, row = j;
-        if (paged) {
-          const int pg = j / a.page_size;
-          row = j - pg * a.page_size;
-          if (seq != p.r || pg < page_base || pg >= page_base + 32) {
-            seq = p.r;
-            page_base = pg;
-            const int mine = pg + lane;
-            page_id = mine < (keys + a.page_size - 1) / a.page_size
-                          ? a.page_table[static_cast<int64_t>(p.r) * a.max_pages + mine]
-                          : -1;
-          }
-          outer = __shfl_sync(0xFFFFFFFFu, page_id, pg - page_base);
-          if (outer < 0 || outer >= a.num_pages) {
-            if (pass == 0 && lane == 0) set_status(status, FP2_DEV_PAGE_OOB);
-            continue;
-          }
-        }
-        if (pass == 0) {
-          const int n = end - j < step ? end - j : step;
-          const uint64_t m = (n == 64 ? ~0ull : (1ull << n) - 1) << ((j - j0) & 63);
-#pragma unroll
-          for (int w = 0; w < TILE / 64; ++w)
-            if (((j - j0) >> 6) == w) ok[w] |= m;
-          bytes += step * D * ELT * (v_smem != 0 ? 2 : 1);
-        } else if (lane == 0 && !withhold) {
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h) {
-            const uint32_t off = h * (TILE * 128) + (j - j0) * 128;
-            tma_load_4d(k_smem + off, &a.tm_k, bar, h * (128 / ELT), g, row, outer);
-            if (v_smem != 0) tma_load_4d(v_smem + off, &a.tm_v, bar, h * (128 / ELT), g, row, outer);
-          }
-        }
-      }
-      if (pass == 0 && lane == 0) {
-#pragma unroll
-        for (int w = 0; w < TILE / 64; ++w) valid[w] = ok[w];
-        if (bytes != 0)
-          mbar_arrive_expect_tx(bar, bytes);
-        else
-          mbar_arrive(bar);
-      }
-    }
-  }
-};
 
 // ------------------------------------------------------------------ operand fragments
 
@@ -270,18 +125,6 @@ FP2_DEVICE void stage_q(const DecodeArgs& a, char* q_smem, int t0, int g, int ro
   }
 }
 
-// Which of the 16 keys from key j a token sees, bit by bit: all below `base` (the first drafted
-// key), of the drafted ones those in its mask.
-FP2_DEVICE uint32_t seen16(uint64_t mask, int j, int base) {
-  const int off = j - base;
-  if (off >= 0) return off < 64 ? static_cast<uint32_t>(mask >> off) & 0xFFFFu : 0u;
-  if (off <= -16) return 0xFFFFu;
-  return static_cast<uint32_t>((mask << -off) | ((1ull << -off) - 1)) & 0xFFFFu;
-}
-FP2_DEVICE uint64_t token_mask(const DecodeArgs& a, int t0, int i) {
-  return a.mask != nullptr ? a.mask[static_cast<int64_t>(t0) + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
-}
-
 // ------------------------------------------------------------------ tree attention
 
 // Rows of a CTA: WM warps x MT tiles of 16; the 64 keys of a tile go to 4 warps, 16 each.
@@ -289,7 +132,7 @@ template <int DT, int D, int MT, int WM>
 struct Tree {
   static constexpr int ELT = DT == 1 ? 2 : 1;
   static constexpr bool F16 = DT == 2;
-  static constexpr int WN = 4, TILE = kTreeTile;
+  static constexpr int WN = 4, TILE = kFewTile;
   static constexpr int ROWS = 16 * MT * WM;
   static constexpr int CONSUMERS = 32 * WM * WN;
   static constexpr int THREADS = CONSUMERS + 32;
@@ -335,7 +178,7 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // K and V
       mbar_init(&empty[s], C::CONSUMERS / 32);
     }
     abort_flag = 0;
@@ -368,8 +211,8 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
           if (!__all_sync(0xFFFFFFFFu, free)) goto drain;
         }
         const uint32_t k_at = smem_u32(stages + s * C::STAGE_BYTES);
-        load.load(a, p, len[p.r], g, t * C::TILE, k_at, k_at + C::KV_BYTES, &full[s], &valid[s],
-                  &status_word, it == a.withhold);
+        load.load(a, &a.tm_k, p.r, len[p.r], g, t * C::TILE, k_at, &full[s], &valid[s], &status_word, it == a.withhold);
+        load.load(a, &a.tm_v, p.r, len[p.r], g, t * C::TILE, k_at + C::KV_BYTES, &full[s], nullptr, &status_word, false);
         ++it;
         if (++s == C::STAGES) s = 0;
       }
@@ -709,7 +552,7 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
               make_float2(top == neg_inf() ? top : top * a.scale_log2 - C::P_BIAS, total);
       }
     }
-    // The group that holds an item's first piece tells combine_kernel how many follow.
+    // The group that holds an item's first piece tells join_kernel how many follow.
     u += p.t1 - p.t0;
     if (g == 0 && tid == 0 && u >= u1) {
       int4 d = make_int4(-1, 0, 0, 0);
@@ -727,19 +570,19 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
 
 // Joins the pieces of an item that several groups worked on, in group order: one warp per row,
 // o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ DecodeArgs a,
-                                                      const __grid_constant__ DecodePlan P) {
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeArgs a,
+                                                   const __grid_constant__ DecodePlan P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
   const int4 d = a.desc[grp];
   if (d.x < 0) return;
   const int rr = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int t0 = P.q_off[d.y], rows = (P.q_off[d.y + 1] - t0) * a.G, m = d.z * ROWS + rr;
+  const int t0 = P.q_off[d.y], rows = (P.q_off[d.y + 1] - t0) * a.G, m = d.z * a.part_rows + rr;
   if (m >= rows) return;
   const auto at = [&](int i) {  // row of piece i in the partial buffers
     const int64_t slot = (static_cast<int64_t>(grp + i) * a.Hkv + g) * 2 + (i == 0 ? d.x : 0);
-    return slot * ROWS + rr;
+    return slot * a.part_rows + rr;
   };
   float top = neg_inf();
   bool any = false;  // some piece saw a key (all of whose scores may be NaN)
@@ -759,7 +602,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ De
     for (int i = 0; i < d.w; ++i) {
       const int64_t row = at(i);
       const float2 ml = a.part_ml[row];
-      const float w = ml.y == 0.f ? 0.f : fast_exp2(ml.x - top);
+      if (ml.y == 0.f) continue;  // saw nothing of the row; its part_o may not even be written
+      const float w = fast_exp2(ml.x - top);
       total += w * ml.y;
       const float* src = a.part_o + row * D + lane * V;
       float x[V];
@@ -786,37 +630,15 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ De
     a.lse[static_cast<int64_t>(h) * a.T + row] = total == 0.f ? neg_inf() : (top + log2f(total)) * kLn2;
 }
 
-template <int DT, int D, int MT, int WM>
-cudaError_t run_tree(const DecodeArgs& a, const DecodePlan& P, int max_rows, cudaStream_t stream) {
-  using C = Tree<DT, D, MT, WM>;
+template <int DT, int D>
+cudaError_t run_tree(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
+  using C = Tree<DT, D, 1, 1>;
   static_assert(C::STAGES >= 2, "tiles must fit twice");
-  const auto kernel = tree_kernel<DT, D, MT, WM>;
-  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
+  const auto kernel = tree_kernel<DT, D, 1, 1>;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   kernel<<<a.groups * a.Hkv, C::THREADS, C::SMEM, stream>>>(a, P);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.groups == 1) return cudaSuccess;  // no item is split
-  // Launched while the attention still runs; griddepcontrol.wait holds it until that has ended.
-  cudaLaunchConfig_t cfg{};
-  const int rows = max_rows < C::ROWS ? max_rows : C::ROWS;
-  cfg.gridDim = dim3(a.groups * a.Hkv, (rows + 3) / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D, C::ROWS>, a, P);
-}
-
-template <int DT, int D>
-cudaError_t run_tree_rows(const DecodeArgs& a, const DecodePlan& P, int max_rows, cudaStream_t stream) {
-  switch (tree_rows(max_rows)) {
-    case 16: return run_tree<DT, D, 1, 1>(a, P, max_rows, stream);
-    case 32: return run_tree<DT, D, 2, 1>(a, P, max_rows, stream);
-    default: return run_tree<DT, D, 2, 2>(a, P, max_rows, stream);
-  }
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -898,8 +720,8 @@ __global__ void __launch_bounds__(Mass<DT, D>::THREADS, 2)
             const bool free = mbar_wait(&empty[s], ((it / stages) & 1) ^ 1, &abort_flag, &status_word, a.wait_limit_ns);
             if (!__all_sync(0xFFFFFFFFu, free)) goto drain;
           }
-          load.load(a, p, len[p.r], g, t * C::TILE, smem_u32(ring + s * C::STAGE_BYTES), 0, &full[s], valid[s],
-                    &status_word, it == a.withhold);
+          load.load(a, &a.tm_k, p.r, len[p.r], g, t * C::TILE, smem_u32(ring + s * C::STAGE_BYTES), &full[s],
+                    valid[s], &status_word, it == a.withhold);
           ++it;
           if (++s == stages) s = 0;
         }
@@ -1055,15 +877,26 @@ cudaError_t run_mass(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stre
 
 }  // namespace
 
-int tree_rows(int max_rows) { return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : 64); }
-int tree_ctas_per_sm(int max_rows) { return tree_rows(max_rows) <= 32 ? 2 : 1; }
-
-cudaError_t launch_tree_attend(int dtype, int D, int max_rows, const DecodeArgs& a, const DecodePlan& P,
-                               cudaStream_t stream) {
-  if (dtype == FP2_BF16 && D == 128) return run_tree_rows<1, 128>(a, P, max_rows, stream);
-  if (dtype == FP2_BF16 && D == 64) return run_tree_rows<1, 64>(a, P, max_rows, stream);
-  if (dtype == FP2_E4M3 && D == 128) return run_tree_rows<2, 128>(a, P, max_rows, stream);
+cudaError_t launch_tree_few(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
+  if (dtype == FP2_BF16 && D == 128) return run_tree<1, 128>(a, P, stream);
+  if (dtype == FP2_BF16 && D == 64) return run_tree<1, 64>(a, P, stream);
+  if (dtype == FP2_E4M3 && D == 128) return run_tree<2, 128>(a, P, stream);
   return cudaErrorInvalidValue;
+}
+
+// Launched while the attention still runs; griddepcontrol.wait holds it until that has ended.
+cudaError_t launch_tree_join(int D, int max_rows, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  const int rows = max_rows < a.part_rows ? max_rows : a.part_rows;
+  cfg.gridDim = dim3(a.groups * a.Hkv, (rows + 3) / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, D == 128 ? join_kernel<128> : join_kernel<64>, a, P);
 }
 
 cudaError_t launch_key_mass(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {

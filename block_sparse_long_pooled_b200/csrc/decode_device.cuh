@@ -1,0 +1,170 @@
+// What the kernels that read a KV cache share: the axis of units that balances a ragged batch, the TMA
+// producer that walks its pages, and the masks of drafted tokens.
+#pragma once
+
+#include "fp2_device.cuh"
+#include "fp2_kernels.h"
+#include "serve_kernels.h"
+
+namespace fp2 {
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------------ small PTX wrappers
+
+FP2_DEVICE void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+FP2_DEVICE float neg_inf() { return __uint_as_float(0xFF800000u); }
+FP2_DEVICE float pos_inf() { return __uint_as_float(0x7F800000u); }
+
+// ------------------------------------------------------------------ the axis of units
+
+// Keys of sequence r, or -1 when its length is no valid one (below its drafted tokens, above
+// max_kv_len): such a sequence has one empty tile and its rows see nothing.
+FP2_DEVICE int seq_keys(const DecodeArgs& a, const DecodePlan& P, int r) {
+  const int n = a.kv_len[r];
+  return (n < P.q_off[r + 1] - P.q_off[r] || n > a.max_kv_len) ? -1 : n;
+}
+
+// Lengths into len[] and the exclusive prefix of the units per sequence into pre[0 .. num_seqs]:
+// units = row tiles (at least least_tiles) * max(1, key tiles).  The whole block reads the lengths at once (one trip to
+// memory whatever the batch), one warp adds up.  Ends with the block synchronised.
+template <int TILE>
+FP2_DEVICE void scan_units(const DecodeArgs& a, const DecodePlan& P, int rows_per_tile, int least_tiles, long long* pre,
+                           int* len, uint32_t* status) {
+  for (int r = threadIdx.x; r < P.num_seqs; r += blockDim.x) {
+    len[r] = seq_keys(a, P, r);
+    if (len[r] < 0) set_status(status, FP2_DEV_LEN_OOB);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    long long run = 0;
+    for (int base = 0; base < P.num_seqs; base += 32) {
+      const int r = base + lane;
+      long long u = 0;
+      if (r < P.num_seqs) {
+        const int rows = (P.q_off[r + 1] - P.q_off[r]) * a.G;
+        const int tiles = len[r] <= 0 ? 1 : (len[r] + TILE - 1) / TILE;
+        u = static_cast<long long>(max((rows + rows_per_tile - 1) / rows_per_tile, least_tiles)) * tiles;
+      }
+      long long inc = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (r < P.num_seqs) pre[r] = run + inc - u;
+      run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+    if (lane == 0) pre[P.num_seqs] = run;
+  }
+  __syncthreads();
+}
+
+// Groups that get a share: no more than there are units.
+FP2_DEVICE int active_groups(long long units, int groups) {
+  return static_cast<int>(units < 1 ? 1 : (units < groups ? units : groups));
+}
+
+// The CTA's status bits go to a word of its own in scratch (see serve_kernels.h); every thread
+// calls it, with nothing of the CTA's left to do.
+FP2_DEVICE void store_status(const DecodeArgs& a, const uint32_t* status) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.scratch[kStatusFirst + blockIdx.x] = *status;
+    if (blockIdx.x == 0) *reinterpret_cast<uint2*>(a.scratch) = make_uint2(0u, kStatusMagic | gridDim.x);
+  }
+}
+
+// ------------------------------------------------------------------ producer
+
+// Brings one tile of TILE keys (from key j0) of K or V into shared memory, page by page, in boxes of
+// 128 bytes x up to 64 rows, and completes `bar`.  Called by a whole warp; the ids of 32 pages at a
+// time sit in the lanes.  `valid` (64 bits a word; may be NULL) tells which rows hold a key of the
+// sequence: rows past its end and rows of a page id out of range do not, and are not loaded.
+template <int TILE, int ELT, int D>
+struct Producer {
+  static constexpr int HALVES = D * ELT / 128;            // boxes side by side
+  int page_base = -1, page_id = -1, seq = -1;             // lanes hold pages page_base .. + 31 of sequence seq
+
+  FP2_DEVICE void load(const DecodeArgs& a, const CUtensorMap* map, int r, int keys, int g, int j0, uint32_t dst,
+                       uint64_t* bar, uint64_t* valid, uint32_t* status, bool withhold) {
+    const int lane = threadIdx.x & 31;
+    const bool paged = a.page_table != nullptr;
+    const int step = paged && a.page_size < 64 ? a.page_size : 64;
+    const int end = keys < j0 + TILE ? keys : j0 + TILE;
+    uint64_t ok[TILE / 64];
+#pragma unroll
+    for (int w = 0; w < TILE / 64; ++w) ok[w] = 0;
+    uint32_t bytes = 0;
+    // First the boxes are counted, then the barrier is armed, then they are issued.
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int j = j0; j < end; j += step) {
+        int outer = r, row = j;
+        if (paged) {
+          const int pg = j / a.page_size;
+          row = j - pg * a.page_size;
+          if (seq != r || pg < page_base || pg >= page_base + 32) {
+            seq = r;
+            page_base = pg;
+            const int mine = pg + lane;
+            page_id = mine < (keys + a.page_size - 1) / a.page_size
+                          ? a.page_table[static_cast<int64_t>(r) * a.max_pages + mine]
+                          : -1;
+          }
+          outer = __shfl_sync(0xFFFFFFFFu, page_id, pg - page_base);
+          if (outer < 0 || outer >= a.num_pages) {
+            if (pass == 0 && lane == 0) set_status(status, FP2_DEV_PAGE_OOB);
+            continue;
+          }
+        }
+        if (pass == 0) {
+          const int n = end - j < step ? end - j : step;
+          const uint64_t m = (n == 64 ? ~0ull : (1ull << n) - 1) << ((j - j0) & 63);
+#pragma unroll
+          for (int w = 0; w < TILE / 64; ++w)
+            if (((j - j0) >> 6) == w) ok[w] |= m;
+          bytes += step * D * ELT;
+        } else if (lane == 0 && !withhold) {
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_4d(dst + h * (TILE * 128) + (j - j0) * 128, map, bar, h * (128 / ELT), g, row, outer);
+        }
+      }
+      if (pass == 0 && lane == 0) {
+        if (valid != nullptr) {
+#pragma unroll
+          for (int w = 0; w < TILE / 64; ++w) valid[w] = ok[w];
+        }
+        if (bytes != 0)
+          mbar_arrive_expect_tx(bar, bytes);
+        else
+          mbar_arrive(bar);
+      }
+    }
+  }
+};
+
+// Which of the 16 keys from key j a token sees, bit by bit: all below `base` (the first drafted
+// key), of the drafted ones those in its mask.
+FP2_DEVICE uint32_t seen16(uint64_t mask, int j, int base) {
+  const int off = j - base;
+  if (off >= 0) return off < 64 ? static_cast<uint32_t>(mask >> off) & 0xFFFFu : 0u;
+  if (off <= -16) return 0xFFFFu;
+  return static_cast<uint32_t>((mask << -off) | ((1ull << -off) - 1)) & 0xFFFFu;
+}
+FP2_DEVICE uint64_t token_mask(const DecodeArgs& a, int t0, int i) {
+  return a.mask != nullptr ? a.mask[static_cast<int64_t>(t0) + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
+}
+
+}  // namespace
+
+}  // namespace fp2

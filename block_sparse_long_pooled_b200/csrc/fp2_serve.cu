@@ -187,7 +187,8 @@ fp2_status run_rotate(const fp2_rotation* p, uint32_t* status_dev, cudaStream_t 
 
 struct DecodeCtx {
   int G = 0, T = 0, max_rows = 0;
-  int groups_tree = 1, groups_mass = 1;
+  bool few = true;                      // which tree attention kernel
+  int part_rows = 16, groups_tree = 1, groups_mass = 1;
   size_t off_desc = 0, off_ml = 0, off_o = 0, bytes = 0;
   float scale = 0.f;
 };
@@ -240,15 +241,19 @@ fp2_status validate(const fp2_decode* p, bool need_v, DecodeCtx& c) {
       return invalid("q_stride_tok must be >= heads * head_dim and a multiple of 16 bytes");
     if (!aligned8(p->tree_mask)) return invalid("tree_mask must be 8-byte aligned");
   }
-  const int sms = num_sms(), rows = fp2::tree_rows(c.max_rows);
-  c.groups_tree = groups_for(p, c.G, fp2::kTreeTile, rows, 0, sms * fp2::tree_ctas_per_sm(c.max_rows));
+  // Two CTAs of the few-rows kernel share an SM, one of the wide kernel fills it.
+  const int sms = num_sms();
+  c.few = c.max_rows <= fp2::kFewRows;
+  c.part_rows = c.few ? fp2::kFewRows : (c.max_rows <= 128 ? 128 : 256);
+  c.groups_tree = c.few ? groups_for(p, c.G, fp2::kFewTile, fp2::kFewRows, 0, sms * 2)
+                        : groups_for(p, c.G, fp2::kWideTile, 128, 0, sms);
   c.groups_mass = groups_for(p, c.G, fp2::kMassTile, FP2_MAX_DRAFT * c.G, 1, sms * 2);
   const size_t ctas = static_cast<size_t>(c.groups_tree) * p->cache.num_kv_heads;
   const size_t words = std::max(ctas, static_cast<size_t>(c.groups_mass) * p->cache.num_kv_heads);
   c.off_desc = FP2_SCRATCH_STATUS_BYTES + align_up(words * 4);
   c.off_ml = c.off_desc + align_up(static_cast<size_t>(c.groups_tree) * 16);
-  c.off_o = c.off_ml + align_up(ctas * 2 * rows * 8);
-  c.bytes = c.off_o + align_up(ctas * 2 * rows * D * 4);
+  c.off_o = c.off_ml + align_up(ctas * 2 * c.part_rows * 8);
+  c.bytes = c.off_o + align_up(ctas * 2 * c.part_rows * D * 4);
   return FP2_OK;
 }
 
@@ -413,7 +418,15 @@ fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void
   a.desc = reinterpret_cast<int4*>(base + c.off_desc);
   a.part_ml = reinterpret_cast<float2*>(base + c.off_ml);
   a.part_o = reinterpret_cast<float*>(base + c.off_o);
-  return launched(fp2::launch_tree_attend(decode->cache.dtype, decode->cache.head_dim, c.max_rows, a, P, st));
+  a.part_rows = c.part_rows;
+  a.v_ptr = decode->cache.v;
+  a.kv_stride = decode->cache.stride_tok;
+  a.kv_stride_outer = decode->cache.stride_outer;
+  const int D = decode->cache.head_dim;
+  FP2_TRY(launched(c.few ? fp2::launch_tree_few(decode->cache.dtype, D, a, P, st)
+                         : fp2::launch_tree_wide(decode->cache.dtype, D, a, P, st)));
+  if (a.groups == 1) return FP2_OK;  // no item is split
+  return launched(fp2::launch_tree_join(D, c.max_rows, a, P, st));
 }
 
 fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, const float* mass_in, float* mass_out,

@@ -77,7 +77,10 @@ struct DecodeArgs {
   float* lse;                 // [Hq, T] or NULL
   int4* desc;                 // [groups] {slot of the first piece of a split item or -1, sequence, row tile, pieces}
   float2* part_ml;            // [groups * Hkv * 2][rows] running maximum (log2 units) and sum
-  float* part_o;              // [groups * Hkv * 2][rows][d]
+  float* part_o;              // [groups * Hkv * 2][part_rows][d]
+  int part_rows;              // rows of a partial result: of an item
+  const void* v_ptr;          // V once more, in elements, for values that the products leave out
+  int64_t kv_stride, kv_stride_outer;
   // key mass
   const float* lse_in;
   const float* mass_in;       // NULL: zero
@@ -91,13 +94,15 @@ struct DecodeArgs {
   int withhold;               // testing: the producer skips the load of this local key tile (-1: none)
 };
 
-// Query rows per CTA of the tree attention kernel for at most max_rows rows per (sequence, KV head).
-int tree_rows(int max_rows);
-int tree_ctas_per_sm(int max_rows);
-cudaError_t launch_tree_attend(int dtype, int D, int max_rows, const DecodeArgs& a, const DecodePlan& P,
-                               cudaStream_t stream);
+// Tree attention kernels: up to kFewRows query rows per (sequence, KV head) decode.cu, above that
+// tree_wide.cu; then the join of the items that several groups share (a.groups > 1).
+constexpr int kFewRows = 16;
+cudaError_t launch_tree_few(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
+cudaError_t launch_tree_wide(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
+cudaError_t launch_tree_join(int D, int max_rows, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
 cudaError_t launch_key_mass(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
-constexpr int kTreeTile = 64;    // keys of a tile of the tree attention kernel
+constexpr int kFewTile = 64;     // keys of a tile: decode.cu
+constexpr int kWideTile = 128;   // tree_wide.cu, which also counts 128 rows as a row tile
 constexpr int kMassTile = 128;   // keys of a tile of the key mass kernel
 
 // ------------------------------------------------------------------ evict
