@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
         }
         const uint32_t k_at = smem_u32(stages + s * C::STAGE_BYTES);
         load.load(a, &a.tm_k, p.r, len[p.r], g, t * C::TILE, k_at, &full[s], &valid[s], &status_word, it == a.withhold);
-        load.load(a, &a.tm_v, p.r, len[p.r], g, t * C::TILE, k_at + C::KV_BYTES, &full[s], nullptr, &status_word, false);
+        load.load(a, &a.tm_v, p.r, len[p.r], g, t * C::TILE, k_at + C::KV_BYTES, &full[s], &valid[s], &status_word, false);
         ++it;
         if (++s == C::STAGES) s = 0;
       }
@@ -599,12 +599,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
   if (__any_sync(0xFFFFFFFFu, any)) {
 #pragma unroll 8
-    for (int i = 0; i < d.w; ++i) {
+    for (int i = 0; i < d.w; ++i) {  // no branch: the loads of eight pieces are in flight at once
       const int64_t row = at(i);
       const float2 ml = a.part_ml[row];
-      if (ml.y == 0.f) continue;  // saw nothing of the row; its part_o may not even be written
-      const float w = fast_exp2(ml.x - top);
-      total += w * ml.y;
       const float* src = a.part_o + row * D + lane * V;
       float x[V];
       if constexpr (V == 4) {
@@ -614,8 +611,12 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
         const float2 v = *reinterpret_cast<const float2*>(src);
         x[0] = v.x, x[1] = v.y;
       }
+      // a piece that saw nothing of the row may not even have written its part_o
+      const bool saw = !(ml.y == 0.f);
+      const float w = saw ? fast_exp2(ml.x - top) : 0.f;
+      total += saw ? w * ml.y : 0.f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += w * x[e];
+      for (int e = 0; e < V; ++e) acc[e] += saw ? w * x[e] : 0.f;
     }
   }
   const int tok = m / a.G, h = g * a.G + (m - tok * a.G);

@@ -87,9 +87,11 @@ FP2_DEVICE void store_status(const DecodeArgs& a, const uint32_t* status) {
 // ------------------------------------------------------------------ producer
 
 // Brings one tile of TILE keys (from key j0) of K or V into shared memory, page by page, in boxes of
-// 128 bytes x up to 64 rows, and completes `bar`.  Called by a whole warp; the ids of 32 pages at a
-// time sit in the lanes.  `valid` (64 bits a word; may be NULL) tells which rows hold a key of the
-// sequence: rows past its end and rows of a page id out of range do not, and are not loaded.
+// 128 bytes x up to 64 rows, and completes `bar`.  Called by a whole warp: lane l looks after box l, and
+// the ids of 32 pages at a time sit in the lanes.  `valid` (64 bits a word) tells which rows hold a key of
+// the sequence: rows past its end and rows of a page id out of range do not, and are not loaded.  (One
+// lane walking the boxes twice, with divisions by the page size, took 1,800 cycles a tile and set the
+// pace of the whole kernel.)
 template <int TILE, int ELT, int D>
 struct Producer {
   static constexpr int HALVES = D * ELT / 128;            // boxes side by side
@@ -99,56 +101,48 @@ struct Producer {
                        uint64_t* bar, uint64_t* valid, uint32_t* status, bool withhold) {
     const int lane = threadIdx.x & 31;
     const bool paged = a.page_table != nullptr;
-    const int step = paged && a.page_size < 64 ? a.page_size : 64;
-    const int end = keys < j0 + TILE ? keys : j0 + TILE;
-    uint64_t ok[TILE / 64];
-#pragma unroll
-    for (int w = 0; w < TILE / 64; ++w) ok[w] = 0;
-    uint32_t bytes = 0;
-    // First the boxes are counted, then the barrier is armed, then they are issued.
-    for (int pass = 0; pass < 2; ++pass) {
-      for (int j = j0; j < end; j += step) {
-        int outer = r, row = j;
-        if (paged) {
-          const int pg = j / a.page_size;
-          row = j - pg * a.page_size;
-          if (seq != r || pg < page_base || pg >= page_base + 32) {
-            seq = r;
-            page_base = pg;
-            const int mine = pg + lane;
-            page_id = mine < (keys + a.page_size - 1) / a.page_size
-                          ? a.page_table[static_cast<int64_t>(r) * a.max_pages + mine]
-                          : -1;
-          }
-          outer = __shfl_sync(0xFFFFFFFFu, page_id, pg - page_base);
-          if (outer < 0 || outer >= a.num_pages) {
-            if (pass == 0 && lane == 0) set_status(status, FP2_DEV_PAGE_OOB);
-            continue;
-          }
-        }
-        if (pass == 0) {
-          const int n = end - j < step ? end - j : step;
-          const uint64_t m = (n == 64 ? ~0ull : (1ull << n) - 1) << ((j - j0) & 63);
-#pragma unroll
-          for (int w = 0; w < TILE / 64; ++w)
-            if (((j - j0) >> 6) == w) ok[w] |= m;
-          bytes += step * D * ELT;
-        } else if (lane == 0 && !withhold) {
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h)
-            tma_load_4d(dst + h * (TILE * 128) + (j - j0) * 128, map, bar, h * (128 / ELT), g, row, outer);
-        }
+    const int step = a.box_rows;                          // a power of two: 64, or the page size below that
+    const int j = j0 + lane * step;
+    bool there = lane * step < TILE && j < keys;
+    int outer = r, row = j;
+    if (paged) {
+      const int first = j0 >> a.page_shift, last = (min(j0 + TILE, keys) - 1) >> a.page_shift;
+      if (keys > j0 && (seq != r || first < page_base || last >= page_base + 32)) {
+        seq = r;
+        page_base = first;
+        page_id = first + lane <= (keys - 1) >> a.page_shift
+                      ? a.page_table[static_cast<int64_t>(r) * a.max_pages + first + lane]
+                      : -1;
       }
-      if (pass == 0 && lane == 0) {
-        if (valid != nullptr) {
-#pragma unroll
-          for (int w = 0; w < TILE / 64; ++w) valid[w] = ok[w];
-        }
-        if (bytes != 0)
-          mbar_arrive_expect_tx(bar, bytes);
-        else
-          mbar_arrive(bar);
+      const int pg = j >> a.page_shift;
+      row = j - (pg << a.page_shift);
+      outer = __shfl_sync(0xFFFFFFFFu, page_id, there ? pg - page_base : 0);
+      if (there && (outer < 0 || outer >= a.num_pages)) {
+        set_status(status, FP2_DEV_PAGE_OOB);
+        there = false;
       }
+    }
+    const uint32_t boxes = __ballot_sync(0xFFFFFFFFu, there);
+    if (lane == 0) {
+      const uint64_t box = step == 64 ? ~0ull : (1ull << step) - 1;
+#pragma unroll
+      for (int w = 0; w < TILE / 64; ++w) {
+        uint64_t ok = 0;
+        for (int b = 0; b < 64; b += step)
+          if ((boxes >> ((64 * w + b) >> a.box_shift)) & 1u) ok |= box << b;
+        const int end = keys - (j0 + 64 * w);             // rows of this word before the sequence's end
+        valid[w] = end >= 64 ? ok : (end <= 0 ? 0 : ok & ((1ull << end) - 1));
+      }
+      if (boxes != 0)
+        mbar_arrive_expect_tx(bar, __popc(boxes) * step * D * ELT);
+      else
+        mbar_arrive(bar);
+    }
+    __syncwarp();  // armed before the first byte arrives
+    if (there && !withhold) {
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+        tma_load_4d(dst + h * (TILE * 128) + lane * step * 128, map, bar, h * (128 / ELT), g, row, outer);
     }
   }
 };

@@ -261,6 +261,8 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+int box_rows(const fp2_cache& c) { return c.page_table != nullptr ? std::min(c.rows, 64) : 64; }
+
 // [outer][token][head][d] with boxes of 128 bytes x up to 64 tokens; a box never leaves its page.
 fp2_status encode_cache(CUtensorMap* m, const fp2_cache& c, void* base) {
   const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(fp2_internal::tensor_map_encoder());
@@ -272,7 +274,7 @@ fp2_status encode_cache(CUtensorMap* m, const fp2_cache& c, void* base) {
       static_cast<cuuint64_t>(c.head_dim) * elt, static_cast<cuuint64_t>(c.stride_tok) * elt,
       static_cast<cuuint64_t>(std::max(c.stride_outer, c.num_outer > 1 ? int64_t(0) : c.stride_tok)) * elt};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / elt), 1u,
-                             static_cast<cuuint32_t>(c.page_table != nullptr ? std::min(c.rows, 64) : 64), 1u};
+                             static_cast<cuuint32_t>(box_rows(c)), 1u};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   const CUresult r = fn(m, c.dtype == FP2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                         base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -292,6 +294,9 @@ fp2_status fill_decode(const fp2_decode* p, const DecodeCtx& c, void* scratch, f
   a.max_kv_len = p->max_kv_len;
   a.page_table = p->cache.page_table;
   a.page_size = p->cache.rows;
+  while (a.page_table != nullptr && (2 << a.page_shift) <= a.page_size) ++a.page_shift;
+  a.box_rows = box_rows(p->cache);
+  while ((2 << a.box_shift) <= a.box_rows) ++a.box_shift;
   a.max_pages = p->cache.max_pages_per_seq;
   a.num_pages = p->cache.num_outer;
   a.mask = p->tree_mask;
@@ -422,6 +427,7 @@ fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void
   a.v_ptr = decode->cache.v;
   a.kv_stride = decode->cache.stride_tok;
   a.kv_stride_outer = decode->cache.stride_outer;
+  if (!c.few && decode->cache.dtype == FP2_E4M3) a.v_descale *= 256.f;  // tree_wide.cu works on V * 2^-8
   const int D = decode->cache.head_dim;
   FP2_TRY(launched(c.few ? fp2::launch_tree_few(decode->cache.dtype, D, a, P, st)
                          : fp2::launch_tree_wide(decode->cache.dtype, D, a, P, st)));

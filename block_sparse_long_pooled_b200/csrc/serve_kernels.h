@@ -66,7 +66,8 @@ struct DecodeArgs {
   const int32_t* kv_len;
   int max_kv_len;
   const int32_t* page_table;  // NULL: token j of sequence r is row j of outer index r
-  int page_size, max_pages, num_pages;
+  int page_size, page_shift, max_pages, num_pages;
+  int box_rows, box_shift;    // rows of a TMA box: 64, or the page size below that
   const uint64_t* mask;       // NULL: causal among the drafted tokens
   int Hq, Hkv, G, T;
   float scale_log2;           // softmax scale * log2(e) * q_descale * k_descale
@@ -102,7 +103,7 @@ cudaError_t launch_tree_wide(int dtype, int D, const DecodeArgs& a, const Decode
 cudaError_t launch_tree_join(int D, int max_rows, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
 cudaError_t launch_key_mass(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
 constexpr int kFewTile = 64;     // keys of a tile: decode.cu
-constexpr int kWideTile = 128;   // tree_wide.cu, which also counts 128 rows as a row tile
+constexpr int kWideTile = 64;    // tree_wide.cu, which also counts 128 rows as a row tile
 constexpr int kMassTile = 128;   // keys of a tile of the key mass kernel
 
 // ------------------------------------------------------------------ evict

@@ -2,17 +2,19 @@
 //
 // The work is cut as in decode.cu (units on one axis, equal shares, partial results joined in group
 // order); only the tile differs.  An M tile is 128 packed rows (token-major, the heads of the group
-// inside) and a key tile 128 keys.  A CTA runs two streams, each with its own S, O and softmax
-// warpgroup, so that the tensor pipe works for one while the other is at its exponentials:
+// inside) and a key tile 64 keys.  A CTA runs two streams, each with its own O and softmax warpgroup:
 //   rows left > 128   ("pair")    stream s has M tile s; both use every key tile that is loaded;
 //   rows left <= 128  ("parity")  both streams have the one M tile, stream s the key tiles with
 //                                 index s mod 2, and their results are merged in shared memory.
 // A pair takes twice a parity tile's time, so a unit is an (M tile, key tile).
 //
-// Per key tile and stream: S = Q K^T into TMEM; one thread per row reads the row's 128 scores,
-// masks them, raises the running maximum only when it grew by more than 2^8 (then O is
-// rescaled in TMEM), and writes P over S in TMEM; O += P V.  Each step needs the one before, hence
-// the two streams.
+// Per key tile and stream: S = Q K^T into TMEM; one thread per row takes the row's 64 scores into
+// registers, masks them, raises the running maximum only when it grew by more than 2^8 (then O is
+// rescaled in TMEM), and writes P over S in TMEM; O += P V.  A stream has two buffers of 64 columns:
+// S(j + 1) is computed while the softmax works on S(j), so that the exponentials, which bound the
+// wide calls (16 a cycle and SM: 512 cycles for 128 x 64, the products take 448), never wait.  With
+// one buffer of 128 keys they stood still for the products of every tile: 299 us against MEASURED us
+// for eight trees of 33 to 64 tokens on an e4m3 cache.
 //
 // P in bf16 would be off by up to 2^-9 of each weight, as much as the output's own rounding; with at
 // most 128 rows the cache's bytes bound the call, so there a second product adds P - bf16(P), for
@@ -35,15 +37,16 @@ struct Wide {
   static constexpr bool E4 = DT == 2;
   static constexpr bool SPLIT = SPLIT_ && !E4;
   static constexpr int ELT = E4 ? 1 : 2;
-  static constexpr int TILE = 128;
+  static constexpr int TILE = kWideTile;
   static constexpr int KCH = 128 / ELT;           // elements of a 128-byte swizzled row
   static constexpr int Q_BYTES = 128 * D * ELT;   // one M tile
   static constexpr int KV_BYTES = TILE * D * ELT; // one K or V tile
   static constexpr int V16_BYTES = E4 ? TILE * D * 2 : 0;
-  static constexpr int STAGES = E4 ? 3 : (D == 64 ? 4 : 2);
+  static constexpr int STAGES = E4 || D == 64 ? 6 : 4;
+  static constexpr int COPIES = 4;                // of V in f16
   static constexpr int KIND_QK = E4 ? 2 : 1, UK = 32 / ELT;
   static constexpr uint32_t FMT_QK = E4 ? 0u : 1u, FMT_PV = E4 ? 0u : 1u;  // e4m3 / bf16; f16 / bf16
-  static constexpr uint32_t IDESC_S = make_idesc(FMT_QK, FMT_QK, 0, 0, 128, 128);
+  static constexpr uint32_t IDESC_S = make_idesc(FMT_QK, FMT_QK, 0, 0, 128, TILE);
   static constexpr uint32_t IDESC_PV = make_idesc(FMT_PV, FMT_PV, 0, 1, 128, D);
   static constexpr float LAZY = 8.f;
   // f16 holds 2^-14 with all its bits: a factor of 2^4 keeps small weights away from the subnormals,
@@ -52,8 +55,8 @@ struct Wide {
   static constexpr int OFF_Q = 0;                              // [2] M tiles
   static constexpr int OFF_K = 2 * Q_BYTES;                    // [STAGES]
   static constexpr int OFF_V = OFF_K + STAGES * KV_BYTES;      // [STAGES]
-  static constexpr int OFF_V16 = OFF_V + STAGES * KV_BYTES;    // [2]
-  static constexpr int OFF_ML = OFF_V16 + 2 * V16_BYTES;       // [128] float2: maximum and sum of stream 1
+  static constexpr int OFF_V16 = OFF_V + STAGES * KV_BYTES;    // [COPIES]
+  static constexpr int OFF_ML = OFF_V16 + COPIES * V16_BYTES;       // [128] float2: maximum and sum of stream 1
   static constexpr int OFF_PRE = OFF_ML + 128 * 8;
   static constexpr int OFF_LEN = OFF_PRE + (FP2_MAX_SEQS + 1) * 8;
   static constexpr int OFF_BAR = (OFF_LEN + FP2_MAX_SEQS * 4 + 15) / 16 * 16;
@@ -81,7 +84,7 @@ FP2_DEVICE WidePiece wide_piece(const long long* pre, const int* len, const Deco
   }
   WidePiece p;
   p.r = lo;
-  p.tiles = len[lo] <= 0 ? 1 : (len[lo] + 127) / 128;
+  p.tiles = len[lo] <= 0 ? 1 : (len[lo] + kWideTile - 1) / kWideTile;
   const int mt = ((P.q_off[lo + 1] - P.q_off[lo]) * a.G + 127) / 128;
   const int rem = static_cast<int>(u - pre[lo]);
   p.rt = rem / (2 * p.tiles);
@@ -109,8 +112,43 @@ FP2_DEVICE void tmem_ld32_now(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 
-// Address of 16-byte chunk c of row k in a tile of 128 rows: 128-byte boxes side by side, swizzled.
-FP2_DEVICE uint32_t box_addr(int k, int c) { return (c >> 3) * (128 * 128) + k * 128 + (((c & 7) ^ (k & 7)) << 4); }
+FP2_DEVICE void tmem_ld64_now(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+      "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+      "%62, %63 }, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+        "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
+        "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+FP2_DEVICE void tmem_ld16_now(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Address of 16-byte chunk c of row k in a tile of ROWS rows: 128-byte boxes side by side, swizzled.
+template <int ROWS>
+FP2_DEVICE uint32_t box_addr(int k, int c) {
+  return (c >> 3) * (ROWS * 128) + k * 128 + (((c & 7) ^ (k & 7)) << 4);
+}
 
 FP2_DEVICE uint4 lds16(uint32_t addr) {
   uint4 v;
@@ -124,9 +162,18 @@ FP2_DEVICE void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// e4m3 to f16 by moving bits: sign, 4 and 3 bits of e4m3 one place lower in a half's top byte are an
+// f16 of 2^-8 times the value, subnormals included (the factor leaves with v_descale).  Three
+// instructions of the integer pipe for two values, where cvt.f16x2.e4m3x2 took 0.9 us a tile of 64 x
+// 128 for the SM's four V warps.  0x7F, NaN in e4m3, becomes a number: those bytes are looked for.
+FP2_DEVICE uint32_t widen_pair(uint32_t t) { return (t & 0x80008000u) | ((t >> 1) & 0x3F803F80u); }
+FP2_DEVICE uint32_t widen_lo(uint32_t w) { return widen_pair(__byte_perm(w, 0, 0x1404)); }
+FP2_DEVICE uint32_t widen_hi(uint32_t w) { return widen_pair(__byte_perm(w, 0, 0x3424)); }
+FP2_DEVICE uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }  // bit 7 of each
+
 // Clears the halves of a word (bf16, exponent all ones) or the bytes (e4m3, 0x7F) that are not finite.
 template <bool E4>
-FP2_DEVICE uint32_t finite_only(uint32_t w, bool& bad) {
+FP2_DEVICE uint32_t finite_only(uint32_t w) {
   uint32_t keep = 0xFFFFFFFFu;
   if constexpr (E4) {
 #pragma unroll
@@ -137,8 +184,39 @@ FP2_DEVICE uint32_t finite_only(uint32_t w, bool& bad) {
     for (int b = 0; b < 2; ++b)
       if (((w >> (16 * b)) & 0x7F80u) == 0x7F80u) keep &= ~(0xFFFFu << (16 * b));
   }
-  bad |= keep != 0xFFFFFFFFu;
   return w & keep;
+}
+
+// Adds what finite_only cleared of the drafted keys in [j0, j1) to one row's result (f32 partial or bf16
+// output), where the row sees the key.  Out of line: it hardly ever runs.
+template <int DT, int D>
+__device__ __noinline__ void add_cleared(const DecodeArgs& a, int r, int g, int base, int q_len, uint64_t mask, int j0,
+                                         int j1, float* part, uint16_t* out) {
+  for (int b = 0; b < q_len; ++b) {
+    const int j = base + b;
+    if (!((mask >> b) & 1) || j < j0 || j >= j1) continue;
+    int64_t outer = r, at = j;
+    if (a.page_table != nullptr) {
+      outer = a.page_table[static_cast<int64_t>(r) * a.max_pages + j / a.page_size];
+      at = j % a.page_size;
+      if (outer < 0 || outer >= a.num_pages) continue;
+    }
+    const int64_t e = outer * a.kv_stride_outer + at * a.kv_stride + static_cast<int64_t>(g) * D;
+    for (int d = 0; d < D; ++d) {
+      float v;
+      if constexpr (DT == 2) {
+        if ((static_cast<const uint8_t*>(a.v_ptr)[e + d] & 0x7Fu) != 0x7Fu) continue;
+        v = __uint_as_float(0x7FFFFFFFu);
+      } else {
+        v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.v_ptr)[e + d]) << 16);
+        if (isfinite(v)) continue;
+      }
+      if (part != nullptr)
+        part[d] += v;
+      else
+        out[d] = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(static_cast<uint32_t>(out[d]) << 16) + v, 0.f));
+    }
+  }
 }
 
 template <int DT, int D, bool SPLIT>
@@ -156,18 +234,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint64_t* k_empty = k_full + C::STAGES;     // both streams are done with it
   uint64_t* v_full = k_empty + C::STAGES;
   uint64_t* v_empty = v_full + C::STAGES;     // bf16: by the MMA issuers; e4m3: by the V warps
-  uint64_t* v_ready = v_empty + C::STAGES;    // V (e4m3: its f16 copy, two of them) can be multiplied
-  uint64_t* v_used = v_ready + C::STAGES;     // [2] e4m3: the copy is free again
-  uint64_t* q_ready = v_used + 2;             // [2] stream s may start the piece's products
-  uint64_t* s_full = q_ready + 2;             // [2]
-  uint64_t* p_full = s_full + 2;              // [2]
-  uint64_t* pv_done = p_full + 2;             // [2]
-  uint64_t* all_done = pv_done + 2;           // [2]
+  uint64_t* v_ready = v_empty + C::STAGES;    // V (e4m3: copy it % COPIES) can be multiplied
+  uint64_t* v_used = v_ready + C::STAGES;     // [COPIES] e4m3: the copy is free again
+  uint64_t* q_ready = v_used + C::COPIES;     // [2] stream s may start the piece's products
+  uint64_t* s_full = q_ready + 2;             // [stream][buffer], as the next two
+  uint64_t* p_full = s_full + 4;
+  uint64_t* pv_done = p_full + 4;
+  uint64_t* all_done = pv_done + 4;           // [2]
   // Which rows of a tile hold keys: valid_v goes with the V stage.  The softmax reads valid_k later than
-  // its K stage is released; when tile x is loaded every stream is past tile x - STAGES - 2.
-  constexpr int VALID = 8;
-  static_assert(VALID >= C::STAGES + 2, "ring of masks");
-  __shared__ uint64_t valid_k[VALID][2], valid_v[C::STAGES][2];
+  // its K stage is released: S(x - STAGES) is issued then, whose buffer the stream's tile two before had
+  // (in parity four tiles before), so everything up to tile x - STAGES - 5 has been read.
+  constexpr int VALID = 16;
+  static_assert(VALID >= C::STAGES + 5, "ring of masks");
+  __shared__ uint64_t valid_k[VALID], valid_v[C::STAGES];
   __shared__ int abort_flag;
   __shared__ int bad_v;                       // some drafted key of this CTA's has a value that is not finite
   __shared__ uint32_t status_word, tmem_slot;
@@ -180,15 +259,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 2);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], C::E4 ? 4 : 2);
-      mbar_init(&v_ready[s], 4);
+      mbar_init(&v_empty[s], C::E4 ? 1 : 2);
+      mbar_init(&v_ready[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&v_used[s], 2);
-      mbar_init(&q_ready[s], 4);
+    for (int s = 0; s < C::COPIES; ++s) mbar_init(&v_used[s], 2);
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4);
       mbar_init(&pv_done[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_ready[s], 4);
       mbar_init(&all_done[s], 1);
     }
     abort_flag = 0;
@@ -217,35 +298,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   };
 
   if (warp >= 8) {
-    if (warp == 8) {
-      // ---------------------------------------------------------------- producer
+    if (warp == 8 || warp == 11) {
+      // ---------------------------------------------------------------- producers: K, V
+      const bool is_k = warp == 8;
+      uint64_t* full = is_k ? k_full : v_full;
+      uint64_t* empty = is_k ? k_empty : v_empty;
+      const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V);
       Producer<C::TILE, C::ELT, D> load;
       int it = 0;
       bool alive = true;
       for (long long u = u0; u < u1 && alive;) {
         const WidePiece p = wide_piece(pre, len, a, P, u, u1);
-        for (int t = p.t0; t < p.t1; ++t) {
+        for (int t = p.t0; t < p.t1; ++t, ++it) {
           const int st = it % C::STAGES, round = it / C::STAGES;
-          if (round > 0 && !(alive = wait(&k_empty[st], (round - 1) & 1))) break;
-          load.load(a, &a.tm_k, p.r, len[p.r], g, t * C::TILE, sbase + C::OFF_K + st * C::KV_BYTES, &k_full[st],
-                    valid_k[it % VALID], &status_word, it == a.withhold);
-          if (round > 0 && !(alive = wait(&v_empty[st], (round - 1) & 1))) {
-            ++it;
-            break;
-          }
-          load.load(a, &a.tm_v, p.r, len[p.r], g, t * C::TILE, sbase + C::OFF_V + st * C::KV_BYTES, &v_full[st],
-                    valid_v[st], &status_word, false);
-          ++it;
+          if (round > 0 && !(alive = wait(&empty[st], (round - 1) & 1))) break;
+          load.load(a, is_k ? &a.tm_k : &a.tm_v, p.r, len[p.r], g, t * C::TILE, ring + st * C::KV_BYTES, &full[st],
+                    is_k ? &valid_k[it % VALID] : &valid_v[st], &status_word, is_k && it == a.withhold);
         }
         u = p.next;
       }
       // Copies in flight end before the CTA does.
       if (*static_cast<volatile int*>(&abort_flag)) {
         volatile int no_abort = 0;
-        for (int i = max(0, it - C::STAGES); i < it; ++i) {
-          mbar_wait(&k_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, &status_word, a.wait_limit_ns / 5);
-          mbar_wait(&v_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, &status_word, a.wait_limit_ns / 5);
-        }
+        for (int i = max(0, it - C::STAGES); i < it; ++i)
+          mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, &status_word, a.wait_limit_ns / 5);
       }
     } else if (warp == 9 || warp == 10) {
       // ---------------------------------------------------------------- MMA issuer of stream s
@@ -258,47 +334,55 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int n = p.t1 - p.t0;
         const bool pair = p.w == 2;
         u = p.next;
-        if (n <= (pair ? 0 : s)) {
-          base += n;
-          continue;
+        const int ns = pair ? n : (n + 1 - s) / 2;  // tiles of this stream
+        if (ns > 0) {
+          if (!(alive = wait(&q_ready[s], nq++ & 1))) break;
+          tc_fence_after();
         }
-        if (!(alive = wait(&q_ready[s], nq++ & 1))) break;
-        tc_fence_after();
         const uint64_t qd = smem_desc_sw128(sbase + C::OFF_Q + (pair ? s : 0) * C::Q_BYTES, 16, 1024);
-        const int step = pair ? 1 : 2;
-        for (int i = pair ? 0 : s, j = 0; i < n; i += step, ++j, ++cs) {
-          const int it = base + i, st = it % C::STAGES, ph = (it / C::STAGES) & 1;
-          if (!(alive = wait(&k_full[st], ph))) break;
-          // P(j - 1), which S(j) overwrites, has been used
-          if (j > 0 && !(alive = wait(&pv_done[s], (cs - 1) & 1))) break;
-          tc_fence_after();
-          const uint64_t kd = smem_desc_sw128(sbase + C::OFF_K + st * C::KV_BYTES, 16, 1024);
+        // S(j), then O += P(j - 1) V
+        for (int j = 0; j <= ns && ns > 0; ++j) {
+          if (j < ns) {
+            const int it = base + (pair ? j : 2 * j + s), st = it % C::STAGES, c = cs + j, b = c & 1;
+            if (!(alive = wait(&k_full[st], (it / C::STAGES) & 1))) break;
+            // P(j - 2), which S(j) overwrites, has been used
+            if (j > 1 && !(alive = wait(&pv_done[2 * s + b], ((c >> 1) - 1) & 1))) break;
+            tc_fence_after();
+            const uint64_t kd = smem_desc_sw128(sbase + C::OFF_K + st * C::KV_BYTES, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < D / C::UK; ++k) {
-            const uint64_t off = ((k * C::UK / C::KCH) * (128 * 128) + (k * C::UK % C::KCH) * C::ELT) >> 4;
-            umma_ss_warp<C::KIND_QK>(s_col, qd + off, kd + off, C::IDESC_S, k > 0 ? 1u : 0u);
+            for (int k = 0; k < D / C::UK; ++k) {
+              const int box = k * C::UK / C::KCH, in = (k * C::UK % C::KCH) * C::ELT;
+              umma_ss_warp<C::KIND_QK>(s_col + b * 64, qd + static_cast<uint64_t>((box * (128 * 128) + in) >> 4),
+                                       kd + static_cast<uint64_t>((box * (C::TILE * 128) + in) >> 4), C::IDESC_S,
+                                       k > 0 ? 1u : 0u);
+            }
+            umma_commit_warp(&s_full[2 * s + b]);
+            umma_commit_warp(&k_empty[st]);
+            if (!pair) umma_commit_warp(&k_empty[st]);
           }
-          umma_commit_warp(&s_full[s]);
-          umma_commit_warp(&k_empty[st]);
-          if (!pair) umma_commit_warp(&k_empty[st]);
-          const int vs = C::E4 ? it & 1 : st;
-          if (!(alive = wait(&v_ready[vs], C::E4 ? (it >> 1) & 1 : ph))) break;
-          if (!(alive = wait(&p_full[s], cs & 1))) break;
-          tc_fence_after();
-          const uint64_t vd = smem_desc_sw128(
-              sbase + (C::E4 ? C::OFF_V16 + vs * C::V16_BYTES : C::OFF_V + st * C::KV_BYTES), C::TILE * 128, 1024);
+          if (j > 0) {
+            const int it = base + (pair ? j - 1 : 2 * (j - 1) + s), st = it % C::STAGES, c = cs + j - 1, b = c & 1;
+            const int vs = C::E4 ? it % C::COPIES : st;
+            if (!(alive = wait(&v_ready[vs], (C::E4 ? it / C::COPIES : it / C::STAGES) & 1))) break;
+            if (!(alive = wait(&p_full[2 * s + b], (c >> 1) & 1))) break;
+            tc_fence_after();
+            const uint64_t vd = smem_desc_sw128(
+                sbase + (C::E4 ? C::OFF_V16 + vs * C::V16_BYTES : C::OFF_V + st * C::KV_BYTES), C::TILE * 128, 1024);
 #pragma unroll
-          for (int part = 0; part < (C::SPLIT ? 2 : 1); ++part) {
+            for (int part = 0; part < (C::SPLIT ? 2 : 1); ++part) {
 #pragma unroll
-            for (int k = 0; k < C::TILE / 16; ++k)
-              umma_ts_warp<1>(o_col, s_col + part * 64 + k * 8, vd + static_cast<uint64_t>((k * 16 * 128) >> 4),
-                              C::IDESC_PV, (part > 0 || k > 0 || j > 0) ? 1u : 0u);
+              for (int k = 0; k < C::TILE / 16; ++k)
+                umma_ts_warp<1>(o_col, s_col + b * 64 + part * 32 + k * 8,
+                                vd + static_cast<uint64_t>((k * 16 * 128) >> 4), C::IDESC_PV,
+                                (part > 0 || k > 0 || j > 1) ? 1u : 0u);
+            }
+            uint64_t* used = C::E4 ? &v_used[vs] : &v_empty[st];
+            umma_commit_warp(used);
+            if (!pair) umma_commit_warp(used);
+            umma_commit_warp(&pv_done[2 * s + b]);
           }
-          uint64_t* used = C::E4 ? &v_used[vs] : &v_empty[st];
-          umma_commit_warp(used);
-          if (!pair) umma_commit_warp(used);
-          umma_commit_warp(&pv_done[s]);
         }
+        cs += ns;
         base += n;
       }
       // No product in flight when the CTA ends.
@@ -306,54 +390,90 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       volatile int no_abort = 0;
       mbar_wait(&all_done[s], 0, &no_abort, &status_word, a.wait_limit_ns / 5);
     } else if (warp >= 12) {
-      // ---------------------------------------------------------------- V: thread = key of the tile
-      const int row = tid - 12 * 32;
+      // ---------------------------------------------------------------- V: a warp per tile, a lane per two keys
+      // (A warp's barriers and fence then wait while the others work.)
       int it = 0;
       bool alive = true;
       for (long long u = u0; u < u1 && alive;) {
         const WidePiece p = wide_piece(pre, len, a, P, u, u1);
         const int keys = len[p.r], base = keys - (P.q_off[p.r + 1] - P.q_off[p.r]);
         for (int t = p.t0; t < p.t1; ++t, ++it) {
-          const int st = it % C::STAGES, ph = (it / C::STAGES) & 1;
-          if (!(alive = wait(&v_full[st], ph))) break;
-          const bool here = (valid_v[st][row >> 6] >> (row & 63)) & 1;
-          const bool drafted = t * C::TILE + row >= base;
+          if ((it & 3) != warp - 12) continue;
+          const int st = it % C::STAGES;
+          if (!(alive = wait(&v_full[st], (it / C::STAGES) & 1))) break;
+          const uint64_t valid = valid_v[st];
           const uint32_t v_at = sbase + C::OFF_V + st * C::KV_BYTES;
           bool bad = false;
           if constexpr (C::E4) {
-            if (it >= 2 && !(alive = wait(&v_used[it & 1], ((it >> 1) - 1) & 1))) break;
-            const uint32_t out = sbase + C::OFF_V16 + (it & 1) * C::V16_BYTES;
+            const int copy = it % C::COPIES, turn = it / C::COPIES;
+            if (turn > 0 && !(alive = wait(&v_used[copy], (turn - 1) & 1))) break;
+            const uint32_t out = sbase + C::OFF_V16 + copy * C::V16_BYTES;
+            const auto widen = [&](int row, int c, uint4 x) {
+              sts16(out + box_addr<C::TILE>(row, 2 * c), make_uint4(widen_lo(x.x), widen_hi(x.x), widen_lo(x.y), widen_hi(x.y)));
+              sts16(out + box_addr<C::TILE>(row, 2 * c + 1),
+                    make_uint4(widen_lo(x.z), widen_hi(x.z), widen_lo(x.w), widen_hi(x.w)));
+            };
+            uint32_t nan = 0;
+            if (valid == ~0ull && (t + 1) * C::TILE <= base) {
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              uint4 x = here ? lds16(v_at + box_addr(row, c)) : make_uint4(0, 0, 0, 0);
-              if (drafted) {
-                x.x = finite_only<true>(x.x, bad);
-                x.y = finite_only<true>(x.y, bad);
-                x.z = finite_only<true>(x.z, bad);
-                x.w = finite_only<true>(x.w, bad);
+              for (int h = 0; h < 2; ++h) {
+                uint4 x[D / 16];
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) x[c] = lds16(v_at + box_addr<C::TILE>(lane + 32 * h, c));
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                  widen(lane + 32 * h, c, x[c]);
+                  nan |= nan_bytes(x[c].x) | nan_bytes(x[c].y) | nan_bytes(x[c].z) | nan_bytes(x[c].w);
+                }
               }
-              sts16(out + box_addr(row, 2 * c),
-                    make_uint4(e4m3x2_to_f16x2(x.x & 0xFFFFu), e4m3x2_to_f16x2(x.x >> 16),
-                               e4m3x2_to_f16x2(x.y & 0xFFFFu), e4m3x2_to_f16x2(x.y >> 16)));
-              sts16(out + box_addr(row, 2 * c + 1),
-                    make_uint4(e4m3x2_to_f16x2(x.z & 0xFFFFu), e4m3x2_to_f16x2(x.z >> 16),
-                               e4m3x2_to_f16x2(x.w & 0xFFFFu), e4m3x2_to_f16x2(x.w >> 16)));
+            } else {
+              nan = 1;
             }
-          } else {
-            if (!here) {
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c) sts16(v_at + box_addr(row, c), make_uint4(0, 0, 0, 0));
-            } else if (drafted) {
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c) {
-                uint4 x = lds16(v_at + box_addr(row, c));
-                bool cut = false;
-                x.x = finite_only<false>(x.x, cut);
-                x.y = finite_only<false>(x.y, cut);
-                x.z = finite_only<false>(x.z, cut);
-                x.w = finite_only<false>(x.w, cut);
-                if (cut) sts16(v_at + box_addr(row, c), x);
-                bad |= cut;
+            if (__any_sync(0xFFFFFFFFu, nan != 0)) {
+              // With the tile's end, drafted keys or a NaN: row by row.
+#pragma unroll 1
+              for (int i = 0; i < 2 * (D / 16); ++i) {
+                const int row = lane + 32 * (i & 1), c = i >> 1;
+                const bool drafted = t * C::TILE + row >= base;
+                uint4 x = (valid >> row) & 1 ? lds16(v_at + box_addr<C::TILE>(row, c)) : make_uint4(0, 0, 0, 0);
+                const uint32_t m[4] = {nan_bytes(x.x), nan_bytes(x.y), nan_bytes(x.z), nan_bytes(x.w)};
+                const bool any = (m[0] | m[1] | m[2] | m[3]) != 0;
+                bad |= any && drafted;
+                if (any && drafted) {
+                  x.x = finite_only<true>(x.x);
+                  x.y = finite_only<true>(x.y);
+                  x.z = finite_only<true>(x.z);
+                  x.w = finite_only<true>(x.w);
+                }
+                widen(row, c, x);
+                if (any && !drafted) {
+#pragma unroll 1
+                  for (int e = 0; e < 16; ++e)
+                    if ((m[e >> 2] >> (8 * (e & 3) + 7)) & 1)
+                      asm volatile("st.shared.u16 [%0], %1;" ::"r"(out + box_addr<C::TILE>(row, 2 * c + (e >> 3)) + 2 * (e & 7)),
+                                   "h"(static_cast<uint16_t>(0x7FFF))
+                                   : "memory");
+                }
+              }
+            }
+          } else if (valid != ~0ull || (t + 1) * C::TILE > base) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              const int row = lane + 32 * h;
+              if (!((valid >> row) & 1)) {
+#pragma unroll 1
+                for (int c = 0; c < D / 8; ++c) sts16(v_at + box_addr<C::TILE>(row, c), make_uint4(0, 0, 0, 0));
+              } else if (t * C::TILE + row >= base) {
+#pragma unroll 1
+                for (int c = 0; c < D / 8; ++c) {
+                  const uint32_t at = v_at + box_addr<C::TILE>(row, c);
+                  const uint4 x0 = lds16(at);
+                  const uint4 x = make_uint4(finite_only<false>(x0.x), finite_only<false>(x0.y), finite_only<false>(x0.z),
+                                             finite_only<false>(x0.w));
+                  const bool cut = x.x != x0.x || x.y != x0.y || x.z != x0.z || x.w != x0.w;
+                  if (cut) sts16(at, x);
+                  bad |= cut;
+                }
               }
             }
           }
@@ -363,7 +483,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (lane == 0) {
             if constexpr (C::E4) {
               mbar_arrive(&v_empty[st]);
-              mbar_arrive(&v_ready[it & 1]);
+              mbar_arrive(&v_ready[it % C::COPIES]);
             } else {
               mbar_arrive(&v_ready[st]);
             }
@@ -385,8 +505,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const bool pair = p.w == 2;
       const int keys = len[p.r], tok0 = P.q_off[p.r], q_len = P.q_off[p.r + 1] - tok0;
       const int rows = q_len * a.G, base = keys - q_len;
-      const int row = p.rt * 256 + (pair ? s * 128 : 0) + rt;    // packed row of the sequence
-      const bool mine = row < rows;
+      // Parity with up to 64 rows: they lie in the M tile twice, and stream 1 takes the copy in rows 64 on,
+      // which other schedulers' warps read.
+      const int left = rows - p.rt * 256, shift = !pair && left <= 64 ? 64 : 0;
+      const int local = pair ? s * 128 + rt : rt - s * shift;    // row of the item that this thread has
+      const int row = p.rt * 256 + local;                        // packed row of the sequence
+      const bool mine = local >= 0 && row < rows;
       const int tok = mine ? row / a.G : 0, h = g * a.G + (mine ? row - tok * a.G : 0);
       const bool busy = __any_sync(0xFFFFFFFFu, mine);
       const int n = p.t1 - p.t0;
@@ -395,12 +519,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // used: this thread has seen the last product of the piece before.
       if (pair || s == 0) {
         const uint32_t q_at = sbase + C::OFF_Q + (pair ? s : 0) * C::Q_BYTES;
+        const int from = p.rt * 256 + (pair ? local : (shift ? rt & 63 : rt));
+        const bool there = from < rows;
+        const int ft = there ? from / a.G : 0, fh = g * a.G + (there ? from - ft * a.G : 0);
         const char* src = static_cast<const char*>(a.q) +
-                          ((static_cast<int64_t>(tok0) + tok) * a.q_stride + static_cast<int64_t>(h) * D) * C::ELT;
+                          ((static_cast<int64_t>(tok0) + ft) * a.q_stride + static_cast<int64_t>(fh) * D) * C::ELT;
 #pragma unroll 8
         for (int c = 0; c < D * C::ELT / 16; ++c)
-          sts16(q_at + box_addr(rt, c),
-                mine ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0));
+          sts16(q_at + box_addr<128>(rt, c),
+                there ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0));
         fence_proxy_async_smem();
       }
       if (pair)
@@ -413,47 +540,48 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint64_t mask = mine ? token_mask(a, tok0, tok) : 0;
       int done = 0;
       for (int i = pair ? 0 : s; i < n; i += pair ? 1 : 2, ++cs, ++done) {
-        const uint64_t* valid = valid_k[(base_it + i) % VALID];
-        if (alive) alive = wait(&s_full[s], cs & 1);
+        const int b = cs & 1;
+        if (alive) alive = wait(&s_full[2 * s + b], (cs >> 1) & 1);
         if (!alive) continue;
         tc_fence_after();
         if (busy) {
+          const uint64_t valid = valid_k[(base_it + i) % VALID];
           const int j0 = (p.t0 + i) * C::TILE;
-          // Twice through the row, 32 scores at a time: all 128 at once would leave the 16 warps' registers.
-          const bool tail = j0 + C::TILE > base || valid[0] != ~0ull || valid[1] != ~0ull;
-          const auto scores = [&](int c, uint32_t (&v)[32]) {
-            tmem_ld32_now(s_at + 32 * c, v);
-            if (tail) {
-              const uint32_t here = static_cast<uint32_t>(valid[c >> 1] >> (32 * (c & 1)));
-              const uint32_t vis = here & (seen16(mask, j0 + 32 * c, base) | (seen16(mask, j0 + 32 * c + 16, base) << 16));
+          uint32_t v[64];
+          tmem_ld64_now(s_at + 64 * b, v);
+          if (j0 + C::TILE > base || valid != ~0ull) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t vis = static_cast<uint32_t>(valid >> (32 * w)) &
+                                   (seen16(mask, j0 + 32 * w, base) | (seen16(mask, j0 + 32 * w + 16, base) << 16));
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!((vis >> e) & 1u)) v[e] = 0xFF800000u;
+                if (!((vis >> e) & 1u)) v[32 * w + e] = 0xFF800000u;
             }
-          };
-          float top[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            scores(c, v);
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                top[x] = fmax3(top[x], __uint_as_float(v[e + 2 * x]), __uint_as_float(v[e + 2 * x + 1]));
           }
+          float top[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = fmaxf(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+#pragma unroll
+          for (int e = 8; e < 64; e += 8)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              top[x] = fmax3(top[x], __uint_as_float(v[e + 2 * x]), __uint_as_float(v[e + 2 * x + 1]));
           const float m_new = fmaxf(m_run, fmax3(top[0], top[1], fmaxf(top[2], top[3])) * s2);
           // The maximum is raised, and O rescaled, when it grew by more than 2^8.
           const bool need = m_new > m_run + C::LAZY;
           if (done > 0 && __any_sync(0xFFFFFFFFu, need)) {
+            // O is whole: the products of the tile before have ended
+            alive = wait(&pv_done[2 * s + (b ^ 1)], ((cs - 1) >> 1) & 1);
+            tc_fence_after();
             const float f = need ? fast_exp2(m_run - m_new) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16_now(o_at + 16 * c, o);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32_now(o_at + 32 * c, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_at + 32 * c, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(o_at + 16 * c, o);
             }
           }
           if (need) {
@@ -463,74 +591,39 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const float off = m_run == neg_inf() ? 0.f : C::P_BIAS - m_run;
           const float2 s22 = make_float2(s2, s2), off2 = make_float2(off, off);
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // P's columns 16 c .. of chunk c lie on scores that have been read; the remainders' do not yet.
-          [[maybe_unused]] uint32_t lo[64];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32], hi[16];
-            scores(c, v);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t hi[16];
+            [[maybe_unused]] uint32_t lo[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s22, off2);
+              const float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(v[32 * c + 2 * e]), __uint_as_float(v[32 * c + 2 * e + 1])), s22, off2);
               const float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
               acc[e & 1] = __fadd2_rn(acc[e & 1], w);
               hi[e] = C::E4 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
               if constexpr (C::SPLIT)
-                lo[16 * c + e] =
-                    pack_bf16x2(w.x - __uint_as_float(hi[e] << 16), w.y - __uint_as_float(hi[e] & 0xFFFF0000u));
+                lo[e] = pack_bf16x2(w.x - __uint_as_float(hi[e] << 16), w.y - __uint_as_float(hi[e] & 0xFFFF0000u));
             }
-            tmem_st16(s_at + 16 * c, hi);
-          }
-          if constexpr (C::SPLIT) {
-            tmem_st32(s_at + 64, *reinterpret_cast<const uint32_t(*)[32]>(&lo[0]));
-            tmem_st32(s_at + 96, *reinterpret_cast<const uint32_t(*)[32]>(&lo[32]));
+            tmem_st16(s_at + 64 * b + 16 * c, hi);
+            if constexpr (C::SPLIT) tmem_st16(s_at + 64 * b + 32 + 16 * c, lo);
           }
           l_run += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
           tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[s]);
+        if (lane == 0) mbar_arrive(&p_full[2 * s + b]);
       }
-      if (done > 0 && alive) alive = wait(&pv_done[s], (cs - 1) & 1);
+      if (done > 0 && alive) alive = wait(&pv_done[2 * s + ((cs - 1) & 1)], ((cs - 1) >> 1) & 1);
       tc_fence_after();
       base_it += n;
 
       // ---------------- epilogue
       const bool any_tile = done > 0 && alive && busy;
-      // Values of drafted keys that V's warps cleared come back here, for the rows that see the key.
-      const bool fix = *static_cast<volatile int*>(&bad_v) != 0 && n > 0 && keys > 0 && p.t1 * C::TILE > base && mine;
-      const auto add_cleared = [&](uint32_t (&o)[32], int c0) {
-        for (int b = 0; b < q_len; ++b) {
-          const int j = base + b, t = j / C::TILE;
-          if (!((mask >> b) & 1) || t < p.t0 || t >= p.t1 || (!pair && ((t - p.t0) & 1) != s)) continue;
-          int64_t outer = p.r, at = j;
-          if (a.page_table != nullptr) {
-            outer = a.page_table[static_cast<int64_t>(p.r) * a.max_pages + j / a.page_size];
-            at = j % a.page_size;
-            if (outer < 0 || outer >= a.num_pages) continue;
-          }
-          const char* src = static_cast<const char*>(a.v_ptr) +
-                            (outer * a.kv_stride_outer + at * a.kv_stride + static_cast<int64_t>(g) * D + c0) * C::ELT;
-#pragma unroll 1
-          for (int q = 0; q < 32 * C::ELT / 4; ++q) {
-            const uint32_t word = reinterpret_cast<const uint32_t*>(src)[q];
-            bool bad = false;
-            finite_only<C::E4>(word, bad);
-            if (!bad) continue;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (e * C::ELT / 4 != q) continue;
-              const uint32_t x = C::E4 ? (word >> (8 * (e & 3))) & 0xFFu : (word >> (16 * (e & 1))) & 0xFFFFu;
-              const bool nonfinite = C::E4 ? (x & 0x7Fu) == 0x7Fu : (x & 0x7F80u) == 0x7F80u;
-              if (nonfinite) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(C::E4 ? 0x7FFFFFFFu : x << 16));
-            }
-          }
-        }
-      };
       const bool whole = p.t0 == 0 && p.t1 == p.tiles;
       const int slot = (grp * a.Hkv + g) * 2 + (nth == 0 ? 0 : 1);
-      const int64_t part_row = static_cast<int64_t>(slot) * a.part_rows + (pair ? s * 128 : 0) + rt;
+      const int64_t part_row = static_cast<int64_t>(slot) * a.part_rows + local;
       const int64_t out_row = static_cast<int64_t>(tok0) + tok;
       const bool store = mine && fp2_check(out_row < a.T && h < a.Hq, &status_word);
       const auto write = [&](uint32_t (&o)[32], int c0, float f) {  // 32 values of this thread's row
@@ -568,7 +661,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
             if (any_tile) tmem_ld32_now(o_at + 32 * c, o);
-            if (fix) add_cleared(o, 32 * c);
             if (store && (n > 0 || whole)) write(o, 32 * c, f);
           }
           if (store) write_stats(m_run, l_run);
@@ -576,11 +668,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       } else {
         // Stream 1 hands its sums and O to stream 0 through the second Q tile, MERGE columns at a time.
         float* buf = reinterpret_cast<float*>(smem + C::OFF_Q + C::Q_BYTES);
-        if (s == 1) ml_smem[rt] = make_float2(m_run, l_run);
+        if (s == 1 && mine) ml_smem[local] = make_float2(m_run, l_run);
         asm volatile("bar.sync 1, 256;" ::: "memory");
         float top = m_run, total = l_run, f0 = 1.f, f1 = 0.f;
         if (s == 0) {
-          const float2 other = ml_smem[rt];
+          const float2 other = mine ? ml_smem[local] : make_float2(neg_inf(), 0.f);
           top = fmaxf(m_run, other.x);
           f0 = l_run == 0.f ? 0.f : fast_exp2(m_run - top);
           f1 = other.y == 0.f ? 0.f : fast_exp2(other.x - top);
@@ -598,9 +690,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = 0u;
               if (any_tile) tmem_ld32_now(o_at + c0 + c, o);
-              if (fix) add_cleared(o, c0 + c);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) buf[(c + e) * 128 + rt] = __uint_as_float(o[e]);
+              for (int e = 0; e < 32; ++e)
+                if (mine) buf[(c + e) * 128 + local] = __uint_as_float(o[e]);
             }
           }
           asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -611,12 +703,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = 0u;
               if (any_tile) tmem_ld32_now(o_at + c0 + c, o);
-              if (fix) add_cleared(o, c0 + c);
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 // a stream that saw nothing of the row leaves zeros
                 float x = l_run == 0.f ? 0.f : __uint_as_float(o[e]) * f0;
-                if (f1 != 0.f) x += buf[(c + e) * 128 + rt] * f1;
+                if (f1 != 0.f) x += buf[(c + e) * 128 + local] * f1;
                 o[e] = __float_as_uint(x);
               }
               if (store) write(o, c0 + c, f);
@@ -626,6 +717,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         if (s == 0 && store) write_stats(top, total);
       }
+      // Values of drafted keys that V's warps cleared come back now, for the rows that see the key.
+      if (*static_cast<volatile int*>(&bad_v) != 0 && keys > 0 && p.t1 * C::TILE > base && store && n > 0 &&
+          (pair || s == 0))
+        add_cleared<DT, D>(a, p.r, g, base, q_len, mask, p.t0 * C::TILE, p.t1 * C::TILE,
+                           whole ? nullptr : a.part_o + part_row * D,
+                           whole ? static_cast<uint16_t*>(a.out) + (out_row * a.Hq + h) * D : nullptr);
       tc_fence_before();
       // The group that holds an item's first piece tells join_kernel how many follow.
       u = p.next;
