@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_launch_next();
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 2);  // K and V
@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
     tma_prefetch_desc(&a.tm_k);
     tma_prefetch_desc(&a.tm_v);
   }
+  grid_wait();
   __syncthreads();
   scan_units<C::TILE>(a, P, C::ROWS, 0, pre, len, &status_word);
   const long long units = pre[P.num_seqs];
@@ -573,7 +574,8 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeArgs a,
                                                    const __grid_constant__ DecodePlan P) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_launch_next();
+  grid_wait();
   const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
   const int4 d = a.desc[grp];
   if (d.x < 0) return;
@@ -638,242 +640,7 @@ cudaError_t run_tree(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stre
   const auto kernel = tree_kernel<DT, D, 1, 1>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
-  kernel<<<a.groups * a.Hkv, C::THREADS, C::SMEM, stream>>>(a, P);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-// ------------------------------------------------------------------ key mass
-
-namespace {
-
-template <int DT, int D>
-struct Mass {
-  static constexpr int ELT = DT == 1 ? 2 : 1;
-  static constexpr bool F16 = DT == 2;
-  static constexpr int TILE = kMassTile, WARPS = 4, CONSUMERS = 32 * WARPS, THREADS = CONSUMERS + 32;
-  static constexpr int STAGE_BYTES = TILE * D * ELT;
-  static constexpr int BUDGET = 113 * 1024;  // two CTAs per SM
-  static constexpr int MAX_STAGES = 6;
-  // Query rows (16-bit, and 8 bytes of statistics) held at once; the rest comes in further passes.
-  static constexpr int fixed(int q_rows) {
-    return 1024 + q_rows * (D * 2 + 8) + (FP2_MAX_SEQS + 1) * 8 + FP2_MAX_SEQS * 4 + 256;
-  }
-  static constexpr int stages(int q_rows) {
-    const int n = (BUDGET - fixed(q_rows)) / STAGE_BYTES;
-    return n > MAX_STAGES ? MAX_STAGES : n;
-  }
-};
-
-// mass'[r, g, j] = decay * mass[r, g, j] + sum over the rows that see key j of exp(q.k_j scale - lse).
-// A CTA owns whole key tiles (all query rows of the head), so every sum is one thread group's, in
-// row order: no atomics.  Four warps, 32 keys each; the K fragments of a warp's keys stay in
-// registers while it walks the query rows in shared memory.
-template <int DT, int D>
-__global__ void __launch_bounds__(Mass<DT, D>::THREADS, 2)
-    mass_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P, int stages) {
-  using C = Mass<DT, D>;
-  extern __shared__ char smem_raw[];
-  char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  char* ring = smem;
-  char* q_smem = ring + stages * C::STAGE_BYTES;
-  float* neg_lse = reinterpret_cast<float*>(q_smem + a.q_rows * D * 2);  // [q_rows] -lse in log2 units
-  long long* pre = reinterpret_cast<long long*>(neg_lse + 2 * a.q_rows);
-  int* len = reinterpret_cast<int*>(pre + FP2_MAX_SEQS + 1);
-  __shared__ uint64_t full[C::MAX_STAGES], empty[C::MAX_STAGES], valid[C::MAX_STAGES][2];
-  __shared__ int abort_flag;
-  __shared__ uint32_t status_word;
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
-  if (tid == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], C::WARPS);
-    }
-    abort_flag = 0;
-    status_word = 0;
-    fence_mbar_init();
-    tma_prefetch_desc(&a.tm_k);
-  }
-  __syncthreads();
-  // All rows of a (sequence, head) count as one row tile, no rows too (its weights still decay):
-  // units are key tiles.
-  scan_units<C::TILE>(a, P, FP2_MAX_DRAFT * a.G, 1, pre, len, &status_word);
-  const long long units = pre[P.num_seqs];
-  const int ng = active_groups(units, a.groups);
-  if (grp >= ng) {
-    store_status(a, &status_word);
-    return;
-  }
-  const long long u0 = units * grp / ng, u1 = units * (grp + 1) / ng;
-
-  if (warp == C::WARPS) {
-    Producer<C::TILE, C::ELT, D> load;
-    int s = 0, it = 0;
-    for (long long u = u0; u < u1;) {
-      const Piece p = piece_at<C::TILE>(pre, len, P.num_seqs, u, u1);
-      const int rows = (P.q_off[p.r + 1] - P.q_off[p.r]) * a.G;
-      for (int c0 = 0; c0 == 0 || c0 < rows; c0 += a.q_rows) {
-        for (int t = p.t0; t < p.t1; ++t) {
-          if (it >= stages) {
-            const bool free = mbar_wait(&empty[s], ((it / stages) & 1) ^ 1, &abort_flag, &status_word, a.wait_limit_ns);
-            if (!__all_sync(0xFFFFFFFFu, free)) goto drain;
-          }
-          load.load(a, &a.tm_k, p.r, len[p.r], g, t * C::TILE, smem_u32(ring + s * C::STAGE_BYTES), &full[s],
-                    valid[s], &status_word, it == a.withhold);
-          ++it;
-          if (++s == stages) s = 0;
-        }
-      }
-      u += p.t1 - p.t0;
-    }
-  drain:
-    if (*static_cast<volatile int*>(&abort_flag)) {
-      volatile int no_abort = 0;
-      for (int i = it > stages ? it - stages : 0; i < it; ++i)
-        mbar_wait(&full[i % stages], (i / stages) & 1, &no_abort, &status_word, a.wait_limit_ns / 5);
-    }
-    store_status(a, &status_word);
-    return;
-  }
-
-  const uint32_t q_base = smem_u32(q_smem);
-  int s = 0, it = 0;
-  bool alive = true;
-  for (long long u = u0; u < u1;) {
-    const Piece p = piece_at<C::TILE>(pre, len, P.num_seqs, u, u1);
-    const int keys = len[p.r], t0 = P.q_off[p.r], q_len = P.q_off[p.r + 1] - t0;
-    const int rows = q_len * a.G, base = keys - q_len;
-    const int had = a.mass_in == nullptr ? 0 : (a.mass_len != nullptr ? a.mass_len[p.r] : keys);
-    for (int c0 = 0; c0 == 0 || c0 < rows; c0 += a.q_rows) {
-      const int n_rows = min(a.q_rows, rows - c0), n16 = (n_rows + 15) / 16;
-      consumer_sync<C::CONSUMERS>();  // every warp is done with the rows before
-      stage_q<DT, D, C::CONSUMERS>(a, q_smem, t0, g, c0, n16 * 16, rows, tid);
-      for (int i = tid; i < n16 * 16; i += C::CONSUMERS) {
-        float x = neg_inf();  // rows that are none, or saw nothing: 2^-inf
-        if (c0 + i < rows) {
-          const int tok = (c0 + i) / a.G, h = g * a.G + (c0 + i - tok * a.G);
-          const float l = a.lse_in[static_cast<int64_t>(h) * a.T + t0 + tok];
-          if (l != neg_inf()) x = -l * 1.4426950408889634f;
-        }
-        neg_lse[i] = x;
-      }
-      consumer_sync<C::CONSUMERS>();
-
-      for (int t = p.t0; t < p.t1; ++t) {
-        if (alive) alive = mbar_wait(&full[s], (it / stages) & 1, &abort_flag, &status_word, a.wait_limit_ns);
-        if (!__all_sync(0xFFFFFFFFu, alive)) {
-          alive = false;
-          ++it;
-          if (++s == stages) s = 0;
-          continue;
-        }
-        const uint32_t k_at = smem_u32(ring + s * C::STAGE_BYTES);
-        const int kw = warp * 32, j0 = t * C::TILE + kw;
-        const uint32_t here = static_cast<uint32_t>(valid[s][warp >> 1] >> ((warp & 1) * 32));
-        // K fragments of 32 keys: [group of 16 values][group of 8 keys]
-        uint32_t kf[D / 16][4][2];
-        if constexpr (!C::F16) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              uint32_t b[4];
-              ldsm4(tile_addr<C::TILE>(k_at, kw + 16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)),
-                    b);
-              kf[k][2 * n][0] = b[0], kf[k][2 * n][1] = b[1], kf[k][2 * n + 1][0] = b[2], kf[k][2 * n + 1][1] = b[3];
-            }
-        } else {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            uint32_t b[4];  // four groups of 8 keys of chunk k
-            ldsm4(tile_addr<C::TILE>(k_at, kw + lane, k), b);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) widen_k(b[n], kf[k][n][0], kf[k][n][1]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        ++it;
-        if (++s == stages) s = 0;
-
-        float col[4][2];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) col[n][0] = col[n][1] = 0.f;
-        const bool tail = j0 + 32 > base;
-        for (int m = 0; m < n16; ++m) {
-          float sc[4][4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            uint32_t qa[4];
-            ldsm4(q_addr<DT, D>(q_base, m * 16 + (lane & 15), 2 * k + (lane >> 4)), qa);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) mma<C::F16>(sc[n], qa, kf[k][n][0], kf[k][n][1]);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int rl = m * 16 + (lane >> 2) + 8 * i;
-            const float off = neg_lse[rl];
-            uint32_t vis = off == neg_inf() ? 0u : 0xFFFFFFFFu;  // also keeps 0 x inf of empty rows out
-            if (tail && vis != 0u) {
-              const uint64_t mk = token_mask(a, t0, (c0 + rl) / a.G);
-              vis = seen16(mk, j0, base) | (seen16(mk, j0 + 16, base) << 16);
-            }
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float x = fast_exp2(fmaf(sc[n][2 * i + e], a.scale_log2, off));
-                col[n][e] += (vis >> (8 * n + 2 * (lane & 3) + e)) & 1u ? x : 0.f;
-              }
-          }
-        }
-        // Sum the eight rows of the warp's lanes; lane q of the first four then holds keys 8n + 2q, + 1.
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) col[n][e] += __shfl_xor_sync(0xFFFFFFFFu, col[n][e], o);
-          }
-        // lane = 4 n' + q writes keys 8 n' + 2 q, + 1 for n' = 0 .. 3
-        float w0 = 0.f, w1 = 0.f;
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          if ((lane >> 2) == n) w0 = col[n][0], w1 = col[n][1];
-        if (lane < 16) {
-          const int64_t at = (static_cast<int64_t>(p.r) * a.Hkv + g) * a.mass_stride;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int jj = 8 * (lane >> 2) + 2 * (lane & 3) + e, j = j0 + jj;
-            if (j >= keys) continue;
-            // A key of a page that is not there keeps its weight; its status bit is set.
-            const float w = (here >> jj) & 1u ? (e ? w1 : w0) : 0.f;
-            const float old = c0 > 0 ? a.mass_out[at + j] : (j < had ? a.mass_in[at + j] * a.decay : 0.f);
-            a.mass_out[at + j] = old + w;
-          }
-        }
-      }
-    }
-    u += p.t1 - p.t0;
-  }
-  store_status(a, &status_word);
-}
-
-template <int DT, int D>
-cudaError_t run_mass(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
-  using C = Mass<DT, D>;
-  const int stages = C::stages(a.q_rows), smem = C::fixed(a.q_rows) + stages * C::STAGE_BYTES;
-  if (stages < 2) return cudaErrorInvalidValue;
-  const auto kernel = mass_kernel<DT, D>;
-  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::BUDGET);
-  if (e != cudaSuccess) return e;
-  kernel<<<a.groups * a.Hkv, C::THREADS, smem, stream>>>(a, P, stages);
-  return cudaGetLastError();
+  return launch_chained(kernel, dim3(a.groups * a.Hkv), C::THREADS, C::SMEM, stream, 1, a, P);
 }
 
 }  // namespace
@@ -885,26 +652,10 @@ cudaError_t launch_tree_few(int dtype, int D, const DecodeArgs& a, const DecodeP
   return cudaErrorInvalidValue;
 }
 
-// Launched while the attention still runs; griddepcontrol.wait holds it until that has ended.
 cudaError_t launch_tree_join(int D, int max_rows, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
   const int rows = max_rows < a.part_rows ? max_rows : a.part_rows;
-  cfg.gridDim = dim3(a.groups * a.Hkv, (rows + 3) / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, D == 128 ? join_kernel<128> : join_kernel<64>, a, P);
-}
-
-cudaError_t launch_key_mass(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
-  if (dtype == FP2_BF16 && D == 128) return run_mass<1, 128>(a, P, stream);
-  if (dtype == FP2_BF16 && D == 64) return run_mass<1, 64>(a, P, stream);
-  if (dtype == FP2_E4M3 && D == 128) return run_mass<2, 128>(a, P, stream);
-  return cudaErrorInvalidValue;
+  return launch_chained(D == 128 ? join_kernel<128> : join_kernel<64>, dim3(a.groups * a.Hkv, (rows + 3) / 4), 128, 0,
+                        stream, 1, a, P);
 }
 
 }  // namespace fp2

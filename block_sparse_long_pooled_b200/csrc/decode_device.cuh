@@ -89,31 +89,58 @@ FP2_DEVICE void store_status(const DecodeArgs& a, const uint32_t* status) {
 // Brings one tile of TILE keys (from key j0) of K or V into shared memory, page by page, in boxes of
 // 128 bytes x up to 64 rows, and completes `bar`.  Called by a whole warp: lane l looks after box l, and
 // the ids of 32 pages at a time sit in the lanes.  `valid` (64 bits a word) tells which rows hold a key of
-// the sequence: rows past its end and rows of a page id out of range do not, and are not loaded.  (One
-// lane walking the boxes twice, with divisions by the page size, took 1,800 cycles a tile and set the
-// pace of the whole kernel.)
+// the sequence: rows past its end and rows of a page id out of range do not, and are not loaded.
+// The warp's instructions follow each other at some five cycles apiece, so their number sets the pace of
+// the whole kernel once a tile takes less than they do: a lane walking the boxes twice, with divisions by
+// the page size, took 1,800 cycles a tile, the general form below still 1,100; whole tiles in boxes of 64
+// rows go a short way of their own.
 template <int TILE, int ELT, int D>
 struct Producer {
   static constexpr int HALVES = D * ELT / 128;            // boxes side by side
   int page_base = -1, page_id = -1, seq = -1;             // lanes hold pages page_base .. + 31 of sequence seq
 
+  FP2_DEVICE void fetch_pages(const DecodeArgs& a, int r, int keys, int first) {
+    const int mine = first + static_cast<int>(threadIdx.x & 31);
+    seq = r;
+    page_base = first;
+    page_id = mine <= (keys - 1) >> a.page_shift ? a.page_table[static_cast<int64_t>(r) * a.max_pages + mine] : -1;
+  }
+
   FP2_DEVICE void load(const DecodeArgs& a, const CUtensorMap* map, int r, int keys, int g, int j0, uint32_t dst,
                        uint64_t* bar, uint64_t* valid, uint32_t* status, bool withhold) {
     const int lane = threadIdx.x & 31;
     const bool paged = a.page_table != nullptr;
+    if (a.box_rows == 64 && j0 + TILE <= keys) {
+      const int j = j0 + (lane & (TILE / 64 - 1)) * 64;
+      int outer = r, row = j;
+      if (paged) {
+        if (seq != r || (j0 >> a.page_shift) < page_base || ((j0 + TILE - 1) >> a.page_shift) >= page_base + 32)
+          fetch_pages(a, r, keys, j0 >> a.page_shift);
+        outer = __shfl_sync(0xFFFFFFFFu, page_id, (j >> a.page_shift) - page_base);
+        row = j & (a.page_size - 1);
+      }
+      if (__all_sync(0xFFFFFFFFu, !paged || static_cast<unsigned>(outer) < static_cast<unsigned>(a.num_pages))) {
+        if (lane == 0) {
+#pragma unroll
+          for (int w = 0; w < TILE / 64; ++w) valid[w] = ~0ull;
+          mbar_arrive_expect_tx(bar, TILE * D * ELT);
+        }
+        __syncwarp();
+        if (lane < TILE / 64 && !withhold) {
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_4d(dst + h * (TILE * 128) + lane * (64 * 128), map, bar, h * (128 / ELT), g, row, outer);
+        }
+        return;
+      }
+    }
     const int step = a.box_rows;                          // a power of two: 64, or the page size below that
     const int j = j0 + lane * step;
     bool there = lane * step < TILE && j < keys;
     int outer = r, row = j;
     if (paged) {
       const int first = j0 >> a.page_shift, last = (min(j0 + TILE, keys) - 1) >> a.page_shift;
-      if (keys > j0 && (seq != r || first < page_base || last >= page_base + 32)) {
-        seq = r;
-        page_base = first;
-        page_id = first + lane <= (keys - 1) >> a.page_shift
-                      ? a.page_table[static_cast<int64_t>(r) * a.max_pages + first + lane]
-                      : -1;
-      }
+      if (keys > j0 && (seq != r || first < page_base || last >= page_base + 32)) fetch_pages(a, r, keys, first);
       const int pg = j >> a.page_shift;
       row = j - (pg << a.page_shift);
       outer = __shfl_sync(0xFFFFFFFFu, page_id, there ? pg - page_base : 0);

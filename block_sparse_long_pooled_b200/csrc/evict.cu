@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int row = blockIdx.x / ranks, r = row / a.Hkv, g = row - r * a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_launch_next();
+  grid_wait();
 
   int n = a.kv_len[r];
   const bool bad = n < 0 || n > a.max_kv_len;
@@ -292,18 +294,7 @@ int evict_cluster(const EvictArgs& a) {
 cudaError_t launch_evict(const EvictArgs& a, int ranks, cudaStream_t stream) {
   const auto kernel = a.row_bytes == 128 ? evict_kernel<8> : evict_kernel<16>;
   if (a.row_bytes != 128 && a.row_bytes != 256) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * a.Hkv * ranks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return launch_chained(kernel, dim3(static_cast<unsigned>(a.num_seqs) * a.Hkv * ranks), kThreads, 0, stream, ranks, a);
 }
 
 }  // namespace fp2

@@ -25,6 +25,12 @@ FP2_DEVICE uint64_t globaltimer_ns() {
 
 FP2_DEVICE void set_status(uint32_t* status, uint32_t bits) { atomicOr(status, bits); }
 
+// A kernel launched with launch_chained may start while the one before it on the stream still runs:
+// everything before grid_wait must leave memory alone that the stream's earlier work touches, and every
+// thread's path must pass it.  grid_launch_next lets the next such kernel start likewise.
+FP2_DEVICE void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+FP2_DEVICE void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Checked builds (FP2_CHECKED=1): an invariant that does not hold sets FP2_DEV_CHECK and the caller
 // skips the guarded access.  Normal builds compile every check away.
 #ifndef FP2_CHECKED

@@ -237,7 +237,8 @@ fp2_status validate(const fp2_decode* p, bool need_v, DecodeCtx& c) {
   if (p->kv_len == nullptr || !aligned4(p->kv_len)) return invalid("kv_len must be a 4-byte aligned pointer");
   if (c.T > 0) {
     if (p->q == nullptr || !aligned16(p->q)) return invalid("q must be a 16-byte aligned pointer");
-    if (p->q_stride_tok < static_cast<int64_t>(p->num_q_heads) * D || (p->q_stride_tok * elt_bytes(p->cache.dtype)) % 16)
+    if (p->q_stride_tok < static_cast<int64_t>(p->num_q_heads) * D || p->q_stride_tok >= (int64_t(1) << 37) ||
+        (p->q_stride_tok * elt_bytes(p->cache.dtype)) % 16)
       return invalid("q_stride_tok must be >= heads * head_dim and a multiple of 16 bytes");
     if (!aligned8(p->tree_mask)) return invalid("tree_mask must be 8-byte aligned");
   }
@@ -247,7 +248,7 @@ fp2_status validate(const fp2_decode* p, bool need_v, DecodeCtx& c) {
   c.part_rows = c.few ? fp2::kFewRows : (c.max_rows <= 128 ? 128 : 256);
   c.groups_tree = c.few ? groups_for(p, c.G, fp2::kFewTile, fp2::kFewRows, 0, sms * 2)
                         : groups_for(p, c.G, fp2::kWideTile, 128, 0, sms);
-  c.groups_mass = groups_for(p, c.G, fp2::kMassTile, FP2_MAX_DRAFT * c.G, 1, sms * 2);
+  c.groups_mass = groups_for(p, c.G, fp2::kMassTile, fp2::kMassRows / c.G * c.G, 1, sms);
   const size_t ctas = static_cast<size_t>(c.groups_tree) * p->cache.num_kv_heads;
   const size_t words = std::max(ctas, static_cast<size_t>(c.groups_mass) * p->cache.num_kv_heads);
   c.off_desc = FP2_SCRATCH_STATUS_BYTES + align_up(words * 4);
@@ -279,6 +280,23 @@ fp2_status encode_cache(CUtensorMap* m, const fp2_cache& c, void* base) {
   const CUresult r = fn(m, c.dtype == FP2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                         base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FP2_OK : fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+}
+
+// [token][head][d] with boxes of 128 bytes x the heads of a group x `tokens`.
+fp2_status encode_q(CUtensorMap* m, const fp2_decode* p, int T, int G, int tokens) {
+  const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(fp2_internal::tensor_map_encoder());
+  if (fn == nullptr) return fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const fp2_cache& c = p->cache;
+  const int elt = elt_bytes(c.dtype);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(p->num_q_heads),
+                              static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.head_dim) * elt, static_cast<cuuint64_t>(p->q_stride_tok) * elt};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = fn(m, c.dtype == FP2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                        const_cast<void*>(p->q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FP2_OK : fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }
 
@@ -451,13 +469,17 @@ fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, const float*
   fp2::DecodePlan P;
   FP2_TRY(fill_decode(decode, c, scratch, a, P));
   a.groups = c.groups_mass;
+  a.pass_tokens = fp2::kMassRows / c.G;
+  if (c.T > 0)
+    FP2_TRY(encode_q(&a.tm_q, decode, c.T, c.G, a.pass_tokens));
+  else
+    a.tm_q = a.tm_k;  // there are no rows to load: see key_mass.cu
   a.lse_in = lse;
   a.mass_in = mass_in;
   a.mass_out = mass_out;
   a.mass_stride = mass_stride;
   a.mass_len = mass_len;
   a.decay = decay;
-  a.q_rows = std::min(std::max(c.max_rows + 15, 16) / 16 * 16, 128);
   return launched(fp2::launch_key_mass(decode->cache.dtype, decode->cache.head_dim, a, P, st));
 }
 

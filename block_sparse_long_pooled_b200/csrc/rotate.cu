@@ -56,6 +56,8 @@ FP2_DEVICE void store8(void* p, const float (&x)[8], float inv) {
 // DIN / DOUT: 0 f32, 1 bf16, 2 e4m3.
 template <int DIN, int DOUT, int D>
 __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
+  grid_launch_next();
+  grid_wait();
   constexpr int TPH = D / 16;                          // threads per head
   constexpr int HPW = 32 / TPH;                        // heads per warp step
   constexpr int EIN = DIN == 0 ? 4 : 2, EOUT = DOUT == 0 ? 4 : (DOUT == 1 ? 2 : 1);
@@ -173,8 +175,7 @@ cudaError_t run_rotate(RotateArgs a, cudaStream_t stream) {
   a.iters = (steps + chunks - 1) / chunks;
   const dim3 grid(static_cast<unsigned>((a.tokens + kRotThreads / 32 - 1) / (kRotThreads / 32)),
                   (steps + a.iters - 1) / a.iters);
-  rotate_kernel<DIN, DOUT, D><<<grid, kRotThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_chained(rotate_kernel<DIN, DOUT, D>, grid, kRotThreads, 0, stream, 1, a);
 }
 
 }  // namespace

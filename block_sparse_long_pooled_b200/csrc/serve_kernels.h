@@ -20,6 +20,28 @@ constexpr uint32_t kStatusMagic = 0x5E000000u;   // low 24 bits: words that foll
 constexpr uint32_t kStatusCount = 0x00FFFFFFu;
 constexpr int kStatusFirst = 256 / 4;            // FP2_SCRATCH_STATUS_BYTES in words
 
+// Launch in clusters of `cluster` CTAs, with programmatic stream serialization: a serving step is a chain
+// of calls of a few microseconds, and the next one's launch and set-up then run under the end of the last.
+template <typename... Args>
+cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                           int cluster, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ------------------------------------------------------------------ rotate
 
 struct RotateArgs {
@@ -61,8 +83,10 @@ struct DecodePlan {
 struct DecodeArgs {
   CUtensorMap tm_k;  // [page or sequence][token][Hkv][d], box {128 B, 1, rows, 1}
   CUtensorMap tm_v;
+  CUtensorMap tm_q;           // key mass: [token][Hq][d], box {128 B, G, pass_tokens}
   const void* q;
   int64_t q_stride;
+  int pass_tokens;            // key mass: tokens of a pass, kMassRows / G
   const int32_t* kv_len;
   int max_kv_len;
   const int32_t* page_table;  // NULL: token j of sequence r is row j of outer index r
@@ -89,7 +113,6 @@ struct DecodeArgs {
   int64_t mass_stride;
   const int32_t* mass_len;    // keys of each sequence that mass_in holds, or NULL: all
   float decay;
-  int q_rows;                 // query rows held in shared memory at once
   uint32_t* scratch;          // status words: see StatusWords
   uint64_t wait_limit_ns;
   int withhold;               // testing: the producer skips the load of this local key tile (-1: none)
@@ -104,7 +127,8 @@ cudaError_t launch_tree_join(int D, int max_rows, const DecodeArgs& a, const Dec
 cudaError_t launch_key_mass(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
 constexpr int kFewTile = 64;     // keys of a tile: decode.cu
 constexpr int kWideTile = 64;    // tree_wide.cu, which also counts 128 rows as a row tile
-constexpr int kMassTile = 128;   // keys of a tile of the key mass kernel
+constexpr int kMassTile = 128;   // key_mass.cu: keys of a tile
+constexpr int kMassRows = 128;   //   and query rows of a pass over them
 
 // ------------------------------------------------------------------ evict
 

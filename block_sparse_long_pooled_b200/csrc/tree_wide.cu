@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_launch_next();
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&k_full[s], 1);
@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  grid_wait();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
@@ -751,8 +752,7 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
   const auto kernel = tree_wide_kernel<DT, D, SPLIT>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
-  kernel<<<a.groups * a.Hkv, kWideThreads, C::SMEM, stream>>>(a, P);
-  return cudaGetLastError();
+  return launch_chained(kernel, dim3(a.groups * a.Hkv), kWideThreads, C::SMEM, stream, 1, a, P);
 }
 
 }  // namespace
