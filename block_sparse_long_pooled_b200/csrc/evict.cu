@@ -8,15 +8,18 @@
 // The weights are read, the kept rows of K and V read and written: bytes bound it, and for short
 // caches the number of dependent steps.  One launch does both parts.  A cluster of 1 to 16 CTAs owns
 // one (sequence, KV head), each rank an equal range of its keys.  Selection is a radix select on the
-// weights' bits in order-preserving form: three histograms (11, 11 and 10 bits) of the keys that
-// agree with the digits found so far, added up in rank 0's shared memory through the cluster, give
-// the exact weight of the last key to keep and how many of its equals are kept.  The weights are
-// read once from HBM and four more times from L2, which costs less than holding them would (a rank's
-// share does not fit in registers at 128K keys).  Ballots in index order then give every kept key
-// its row; ranks know the counts of the ranks before them, so nothing depends on timing.  After that
-// the rows are moved, each rank an equal share of the output rows whatever range they came from:
-// the addresses of 512 rows at a time are looked up first, so that the copies themselves wait only
-// for their data.
+// weights' bits in order-preserving form: up to three histograms (11, 11 and 10 bits) of the keys that
+// agree with the digits found so far give the weight of the last key to keep and how many of its equals
+// are kept; it ends early when a digit's keys are all kept.  Each rank publishes its histogram and the
+// sums of 64 groups of 32 bins; warp q of every rank reads rank q's groups, then its 32 bins of the one
+// group that matters: one cluster barrier a digit, little traffic, one trip to another SM at a time.
+// (Adding the histograms up in rank 0 cost 6 us a digit for 16 ranks, one warp reading all ranks 5.)
+// Weights of zero, in earnest the most frequent one, are counted by ballot: one shared-memory add a
+// warp instead of one a key on the same word.  Up to 16 keys a thread stay in registers in between (8,192 a rank); longer ranges are
+// read again from L2.  Ballots in index order then give every kept key its row; ranks know the counts
+// of the ranks before them, so nothing depends on timing.  After that the rows are moved, each rank an
+// equal share of the output rows whatever range they came from: the addresses of 512 rows at a time are
+// looked up first, so that the copies themselves wait only for their data.
 #include <cooperative_groups.h>
 
 #include "fp2_device.cuh"
@@ -29,7 +32,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048, kGroups = kBins / 32, kMaxRanks = 16;
+constexpr int kHeld = 16;         // keys a thread holds
 constexpr int kChunk = kThreads;  // rows whose addresses are looked up at a time
 
 // Weights in an order that unsigned comparison follows.  -0 equals 0; NaN counts as the heaviest.
@@ -41,10 +45,10 @@ FP2_DEVICE uint32_t ordered(float f) {
 }
 
 struct EvictShared {
-  uint32_t local[kBins];      // this rank's histogram
-  uint32_t total[3][kBins];   // the cluster's, in rank 0
-  uint32_t scan[kWarps];
-  uint32_t found[2];          // digit, and how many of the keys above it are still wanted
+  uint32_t bins[3][kBins];    // this rank's histograms
+  uint32_t groups[3][kGroups];
+  uint32_t got[kMaxRanks][kGroups];  // groups, then bins, of every rank
+  uint32_t got_bins[kMaxRanks][32];
   uint32_t count[2];          // of this rank: keys kept outright, keys equal to the threshold
   uint32_t warp_sel[kWarps], warp_eq[kWarps];
   int64_t from[kChunk], to[kChunk];
@@ -92,6 +96,12 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     mass_out[i] = 0.f;
   }
 
+  const auto sync = [&] {
+    if (ranks > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
   if (N == n) {
     // nothing is dropped
     __syncthreads();
@@ -106,110 +116,147 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     const int last = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / ranks);
     const int w0 = first + static_cast<int>(static_cast<int64_t>(last - first) * warp / kWarps);
     const int w1 = first + static_cast<int>(static_cast<int64_t>(last - first) * (warp + 1) / kWarps);
+    const bool held = w1 - w0 <= kHeld;  // every key of this warp's stays in registers
 
-    for (int i = tid; i < 3 * kBins; i += kThreads) (&s.total[0][0])[i] = 0;
+    uint32_t u[kHeld];
+    const auto fetch = [&](int t0) {  // steps t0 .. of this warp, all loads on their way at once
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int j = (t0 + i) * 32 + lane;
+        u[i] = t0 + i < w1 && j < n ? __float_as_uint(__ldg(mass + j)) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) u[i] = ordered(__uint_as_float(u[i]));
+    };
+    fetch(w0);
+    for (int i = tid; i < 3 * kBins; i += kThreads) (&s.bins[0][0])[i] = 0;
     uint32_t need = static_cast<uint32_t>(a.budget - a.sink - a.window);  // of the competing keys
     uint32_t prefix = 0, mask = 0;
-    cluster.sync();
+    __syncthreads();
     // need == 0: no competing key stays, and no key's order value exceeds this threshold.
-    if (need == 0) prefix = 0xFFFFFFFFu;
-    if (need != 0) {
+    bool done = need == 0;
+    if (done) prefix = 0xFFFFFFFFu;
 #pragma unroll 1
-      for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-        const uint32_t digit = pass == 2 ? 1023u : 2047u;
-        for (int i = tid; i < kBins; i += kThreads) s.local[i] = 0;
-        __syncthreads();
-        const int j1 = min(last * 32, free1);
-#pragma unroll 4
-        for (int j = max(first * 32, free0) + tid; j < j1; j += kThreads) {
-          const uint32_t u = ordered(__ldg(mass + j));
-          if ((u & mask) == prefix) atomicAdd(&s.local[(u >> shift) & digit], 1u);
-        }
-        __syncthreads();
-        uint32_t* total = cluster.map_shared_rank(&s.total[pass][0], 0);
-        for (int i = tid; i < kBins; i += kThreads)
-          if (s.local[i] != 0) atomicAdd(total + i, s.local[i]);
-        cluster.sync();
-        // Bins from the heaviest down: thread t holds bins 2047 - 4t .. 2044 - 4t.
-        uint32_t c[4], sum = 0;
+    for (int pass = 0; pass < 3 && !done; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+      uint32_t* mine = s.bins[pass];
+#pragma unroll 1
+      for (int t0 = w0; t0 < w1; t0 += kHeld) {
+        if (!held) fetch(t0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c[e] = total[kBins - 1 - 4 * tid - e];
-          sum += c[e];
+        for (int i = 0; i < kHeld; ++i) {
+          if (t0 + i >= w1) break;
+          const int j = (t0 + i) * 32 + lane;
+          const bool counts = j >= free0 && j < free1 && (u[i] & mask) == prefix;
+          const bool zero = counts && u[i] == 0x80000000u;
+          const uint32_t zeros = __ballot_sync(0xFFFFFFFFu, zero);
+          if (counts && (!zero || (zeros & ((1u << lane) - 1)) == 0))
+            atomicAdd(&mine[(u[i] >> shift) & digit], zero ? static_cast<uint32_t>(__popc(zeros)) : 1u);
         }
-        uint32_t inc = sum;
+      }
+      __syncthreads();
+      {
+        // thread t: bins 4t .. 4t + 3; eight threads a group
+        const uint4 four = *reinterpret_cast<const uint4*>(mine + 4 * tid);
+        uint32_t sum = (four.x + four.y) + (four.z + four.w);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if ((lane & 7) == 0) s.groups[pass][tid >> 3] = sum;
+      }
+      sync();
+      // From the heaviest down: lane l has groups 63 - 2l and 62 - 2l, then bin 31 - l of the group.  Every
+      // warp comes to the same answer from all ranks' counts.
+      const auto before = [&](uint32_t x) {  // sum of the lanes below
+        uint32_t inc = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
           if (lane >= o) inc += v;
         }
-        if (lane == 31) s.scan[warp] = inc;
+        return inc - x;
+      };
+      if (ranks > 1 && warp < ranks)
+        *reinterpret_cast<uint2*>(&s.got[warp][2 * lane]) =
+            *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s.groups[pass][2 * lane], warp));
+      if (ranks > 1) __syncthreads();
+      uint32_t g0 = 0, g1 = 0;
+      for (int q = 0; q < ranks; ++q) {
+        const uint2 x = *reinterpret_cast<const uint2*>(ranks > 1 ? &s.got[q][kGroups - 2 - 2 * lane]
+                                                                  : &s.groups[pass][kGroups - 2 - 2 * lane]);
+        g0 += x.y;
+        g1 += x.x;
+      }
+      uint32_t above = before(g0 + g1);
+      // The one group, then the one bin, in which the need-th key lies (need is at most all of them).
+      const int from = __ffs(__ballot_sync(0xFFFFFFFFu, above < need && above + g0 + g1 >= need)) - 1;
+      const bool second = __shfl_sync(0xFFFFFFFFu, above + g0 < need, from);
+      const uint32_t left = need - __shfl_sync(0xFFFFFFFFu, second ? above + g0 : above, from);
+      const int group = kGroups - 1 - 2 * from - (second ? 1 : 0);
+      if (ranks > 1) {
+        if (warp < ranks) s.got_bins[warp][lane] = *cluster.map_shared_rank(&mine[group * 32 + lane], warp);
         __syncthreads();
-        uint32_t before = inc - sum;
-        for (int w = 0; w < warp; ++w) before += s.scan[w];
-        // The one bin in which the need-th key lies (need is at most the number of keys counted).
-        if (before < need && before + sum >= need) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (before < need && before + c[e] >= need) {
-              s.found[0] = kBins - 1 - 4 * tid - e;
-              s.found[1] = need - before;
-            }
-            before += c[e];
-          }
-        }
-        __syncthreads();
-        prefix |= s.found[0] << shift;
-        mask |= digit << shift;
-        need = s.found[1];
-        __syncthreads();
+      }
+      uint32_t x = 0;
+      for (int q = 0; q < ranks; ++q) x += ranks > 1 ? s.got_bins[q][31 - lane] : mine[group * 32 + 31 - lane];
+      above = before(x);
+      const int at = __ffs(__ballot_sync(0xFFFFFFFFu, above < left && above + x >= left)) - 1;
+      prefix |= static_cast<uint32_t>(group * 32 + 31 - at) << shift;
+      mask |= digit << shift;
+      need = left - __shfl_sync(0xFFFFFFFFu, above, at);
+      if (need == __shfl_sync(0xFFFFFFFFu, x, at)) {
+        // All keys with these digits stay: the threshold is the value before them (no weight maps to 0).
+        prefix -= 1;
+        need = 0;
+        done = true;
       }
     }
     // Keys above `prefix` stay, and of those equal to it the first `need`.
-    const auto classify = [&](int j, bool& keep, bool& tie) {
-      keep = tie = false;
-      if (j >= n) return;
-      if (j < free0 || j >= free1) {
-        keep = true;
-        return;
-      }
-      const uint32_t u = ordered(__ldg(mass + j));
-      keep = u > prefix;
-      tie = u == prefix;
+    const auto classify = [&](int i, int t, bool& keep, bool& tie) {
+      const int j = t * 32 + lane;
+      const bool competes = j >= free0 && j < free1;
+      keep = j < n && (!competes || u[i] > prefix);
+      tie = competes && u[i] == prefix;
     };
     uint32_t sel = 0, eq = 0;
-#pragma unroll 4
-    for (int t = w0; t < w1; ++t) {
-      bool keep, tie;
-      classify(t * 32 + lane, keep, tie);
-      sel += __popc(__ballot_sync(0xFFFFFFFFu, keep));
-      eq += __popc(__ballot_sync(0xFFFFFFFFu, tie));
+#pragma unroll 1
+    for (int t0 = w0; t0 < w1; t0 += kHeld) {
+      if (!held) fetch(t0);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        if (t0 + i >= w1) break;
+        bool keep, tie;
+        classify(i, t0 + i, keep, tie);
+        sel += __popc(__ballot_sync(0xFFFFFFFFu, keep));
+        eq += __popc(__ballot_sync(0xFFFFFFFFu, tie));
+      }
     }
     if (lane == 0) {
       s.warp_sel[warp] = sel;
       s.warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
-      uint32_t x = 0, y = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        x += s.warp_sel[w];
-        y += s.warp_eq[w];
+    uint32_t sel_before = lane < warp ? s.warp_sel[lane & (kWarps - 1)] : 0u;
+    uint32_t eq_before = lane < warp ? s.warp_eq[lane & (kWarps - 1)] : 0u;
+    if (ranks > 1) {
+      if (warp == 0) {
+        uint32_t x = lane < kWarps ? s.warp_sel[lane] : 0u, y = lane < kWarps ? s.warp_eq[lane] : 0u;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+          y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
+        }
+        if (lane == 0) {
+          s.count[0] = x;
+          s.count[1] = y;
+        }
       }
-      s.count[0] = x;
-      s.count[1] = y;
-    }
-    cluster.sync();
-    uint32_t sel_before = 0, eq_before = 0;
-    for (int q = lane; q < rank; q += 32) {
-      const uint32_t* c = cluster.map_shared_rank(&s.count[0], q);
-      sel_before += c[0];
-      eq_before += c[1];
-    }
-    for (int w = lane; w < warp; w += 32) {
-      sel_before += s.warp_sel[w];
-      eq_before += s.warp_eq[w];
+      cluster.sync();
+      if (lane < rank) {  // (up to 16 ranks)
+        const uint32_t* c = cluster.map_shared_rank(&s.count[0], lane);
+        sel_before += c[0];
+        eq_before += c[1];
+      }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -217,24 +264,30 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
       eq_before += __shfl_xor_sync(0xFFFFFFFFu, eq_before, o);
     }
     const uint32_t below = (1u << lane) - 1;
-#pragma unroll 2
-    for (int t = w0; t < w1; ++t) {
-      const int j = t * 32 + lane;
-      bool keep, tie;
-      classify(j, keep, tie);
-      const uint32_t ks = __ballot_sync(0xFFFFFFFFu, keep), es = __ballot_sync(0xFFFFFFFFu, tie);
-      const uint32_t eq_at = eq_before + __popc(es & below);
-      const uint32_t taken = eq_at < need ? eq_at : need;  // ties kept before this key
-      const uint32_t pos = sel_before + __popc(ks & below) + taken;
-      if ((keep || (tie && eq_at < need)) && fp2_check(pos < static_cast<uint32_t>(a.budget), &s.status)) {
-        kept[pos] = j;
-        mass_out[pos] = mass[j];
+#pragma unroll 1
+    for (int t0 = w0; t0 < w1; t0 += kHeld) {
+      if (!held) fetch(t0);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        if (t0 + i >= w1) break;
+        bool keep, tie;
+        classify(i, t0 + i, keep, tie);
+        const uint32_t ks = __ballot_sync(0xFFFFFFFFu, keep), es = __ballot_sync(0xFFFFFFFFu, tie);
+        const uint32_t eq_at = eq_before + __popc(es & below);
+        const uint32_t pos = sel_before + __popc(ks & below) + min(eq_at, need);  // (ties kept before this key)
+        if ((keep || (tie && eq_at < need)) && fp2_check(pos < static_cast<uint32_t>(a.budget), &s.status)) {
+          const int j = (t0 + i) * 32 + lane;
+          kept[pos] = j;
+          // the weight back from its order (no load to wait for; a NaN's own bits are read again)
+          mass_out[pos] = u[i] == 0xFFFFFFFFu ? __ldg(mass + j)
+                                              : __uint_as_float(u[i] & 0x80000000u ? u[i] & 0x7FFFFFFFu : ~u[i]);
+        }
+        sel_before += __popc(ks);
+        eq_before += __popc(es);
       }
-      sel_before += __popc(ks);
-      eq_before += __popc(es);
     }
   }
-  cluster.sync();  // kept[] is complete, and no rank reads another's shared memory from here on
+  sync();  // kept[] is complete, and no rank reads another's shared memory from here on
 
   const int i0 = static_cast<int>(static_cast<int64_t>(N) * rank / ranks);
   const int i1 = static_cast<int>(static_cast<int64_t>(N) * (rank + 1) / ranks);
@@ -282,18 +335,24 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
 
 }  // namespace
 
-// Ranks per cluster: enough that the rows fill the GPU twice over (two CTAs fit on an SM), as long as
-// a rank keeps a thousand keys to look through or to move.
+// Ranks per cluster: so many that the threads can hold a rank's keys (16 x 512), and more for few rows,
+// as long as a rank keeps five hundred keys.  More than 8 need the attribute for clusters beyond the
+// portable size.
 int evict_cluster(const EvictArgs& a) {
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.Hkv;
   int c = 1;
-  while (c < 8 && rows * c < 2 * 148 && a.max_kv_len / (2 * c) >= 1024) c *= 2;
+  while (c < kMaxRanks && (a.max_kv_len > c * kHeld * kThreads || (rows * c < 148 && a.max_kv_len >= 1024 * c))) c *= 2;
   return c;
 }
 
 cudaError_t launch_evict(const EvictArgs& a, int ranks, cudaStream_t stream) {
   const auto kernel = a.row_bytes == 128 ? evict_kernel<8> : evict_kernel<16>;
   if (a.row_bytes != 128 && a.row_bytes != 256) return cudaErrorInvalidValue;
+  if (ranks > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   return launch_chained(kernel, dim3(static_cast<unsigned>(a.num_seqs) * a.Hkv * ranks), kThreads, 0, stream, ranks, a);
 }
 
