@@ -13,8 +13,11 @@
 // One pass over memory: a thread owns 16 values of a head as two vectors of 8 that hold whole pairs
 // ((8c.., rot/2 + 8c..) in the half layout, 16 neighbours in the interleaved one), so no value
 // crosses threads and in-place calls are safe; d / 16 threads share a head's norm by shuffles.  A
-// warp walks the heads of one token, so the eight sines and cosines of a thread serve all of them;
-// with few tokens the heads are spread over more warps instead (launch_rotate).
+// warp walks the heads of one token, first Q's, then K's, then V's.  Bytes should bound it, but at 335
+// million values the instructions count as much: norm weight, cosine and sine are multiplied once per
+// token into four factors a pair, so that a head costs a thread two products, two fused ones and the
+// norm's factor for each pair, in packed fp32 pairs.  With few tokens the heads are spread over more
+// warps instead (run_rotate).
 #include "fp2_device.cuh"
 #include "serve_kernels.h"
 
@@ -23,14 +26,21 @@ namespace fp2 {
 namespace {
 
 constexpr int kRotThreads = 128;
+#ifndef MINB
+#define MINB 7
+#endif
 
-FP2_DEVICE void load8(const void* p, bool f32, float (&x)[8]) {
-  if (f32) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// Eight values: four words of two bf16, or eight floats, from shared or global memory.
+template <int DIN>
+FP2_DEVICE void load8(const char* p, float (&x)[8]) {
+  const uint4 a = reinterpret_cast<const uint4*>(p)[0];
+  if constexpr (DIN == 0) {
+    const uint4 b = reinterpret_cast<const uint4*>(p)[1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
   } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[2 * e] = __uint_as_float(w[e] << 16);
@@ -38,9 +48,18 @@ FP2_DEVICE void load8(const void* p, bool f32, float (&x)[8]) {
     }
   }
 }
-
+FP2_DEVICE uint32_t four_e4m3(float a, float b, float c, float d) {  // a in the lowest byte, saturating
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
 template <int DOUT>
-FP2_DEVICE void store8(void* p, const float (&x)[8], float inv) {
+FP2_DEVICE void store8(char* p, const float (&x)[8]) {
   if constexpr (DOUT == 0) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -48,18 +67,23 @@ FP2_DEVICE void store8(void* p, const float (&x)[8], float inv) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   } else {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                                              pack_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+    *reinterpret_cast<uint2*>(p) = make_uint2(four_e4m3(x[0], x[1], x[2], x[3]), four_e4m3(x[4], x[5], x[6], x[7]));
   }
 }
 
+FP2_DEVICE void copy16(void* to, const char* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+
 // DIN / DOUT: 0 f32, 1 bf16, 2 e4m3.
-template <int DIN, int DOUT, int D>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
+template <int DIN, int DOUT, int D, bool INTER>
+__global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kernel(const __grid_constant__ RotateArgs a) {
   grid_launch_next();
   grid_wait();
   constexpr int TPH = D / 16;                          // threads per head
   constexpr int HPW = 32 / TPH;                        // heads per warp step
+  // A warp's four factors a pair: in shared memory, as 32 registers more would halve the warps per SM.
+  __shared__ __align__(16) float factors[kRotThreads / 32][4][2][TPH][4];
   constexpr int EIN = DIN == 0 ? 4 : 2, EOUT = DOUT == 0 ? 4 : (DOUT == 1 ? 2 : 1);
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRotThreads / 32) + (threadIdx.x >> 5);
@@ -68,106 +92,250 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
   const int half = a.rot >> 1;
   // The two vectors of 8 values: whole pairs of the rotated part, or 16 values of the rest.
   const bool rotated = 16 * p < a.rot;
-  const bool split = rotated && !a.interleaved;
+  const bool split = rotated && !INTER;
   const int e0 = split ? 8 * p : 16 * p, e1 = split ? half + 8 * p : 16 * p + 8;
 
-  float cs[8], sn[8];
-  if (rotated) {
-    const int64_t pos = a.positions[t];
+  // Steps of this warp: HPW heads each, Q's first.
+  const int sq = (a.Hq + HPW - 1) / HPW, sk = (a.Hkv + HPW - 1) / HPW, sv = (a.Hv + HPW - 1) / HPW;
+  const int begin = blockIdx.y * a.iters, end = min(begin + a.iters, sq + sk + sv);
+
+  // Values come through shared memory, AHEAD steps before they are needed and across Q, K and V: in
+  // registers, one step ahead, the loads left the SM waiting.  Every lane reads back what it copied.
+  constexpr int AHEAD = 4, VECS = EIN / 2;             // 16-byte copies of a vector of 8
+  __shared__ __align__(16) char ring[kRotThreads / 32][AHEAD][2 * VECS][32][16];
+  char(*const slots_at)[2 * VECS][32][16] = ring[threadIdx.x >> 5];
+  // The next step to ask for: its section's end, this lane's head in it, and its two vectors.
+  int ask = begin, ask_end = 0, ask_head = 0, ask_heads = 0;
+  const char *ask0 = nullptr, *ask1 = nullptr;
+  const auto request = [&]() {
+    if (ask < end) {
+      if (ask >= ask_end) {
+        const int which = ask < sq ? 0 : (ask < sq + sk ? 1 : 2);
+        const int base = which == 0 ? 0 : (which == 1 ? sq : sq + sk);
+        ask_end = which == 0 ? sq : (which == 1 ? sq + sk : sq + sk + sv);
+        ask_heads = which == 0 ? a.Hq : a.Hkv;
+        ask_head = (ask - base) * HPW + lane / TPH;
+        const char* at = static_cast<const char*>(which == 0 ? a.q : (which == 1 ? a.k : a.v)) +
+                         (t * (which == 0 ? a.q_stride : (which == 1 ? a.k_stride : a.v_stride)) +
+                          static_cast<int64_t>(ask_head) * D) * EIN;
+        ask0 = at + (which == 2 ? 16 * p : e0) * EIN;
+        ask1 = at + (which == 2 ? 16 * p + 8 : e1) * EIN;
+      }
+      // (a lane past the last head works on what its slot holds and stores nothing)
+      if (ask_head < ask_heads) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t turn = static_cast<uint32_t>((static_cast<uint64_t>(pos) * a.phase[8 * p + i]) >> 32);
+        for (int v = 0; v < VECS; ++v) {
+          copy16(slots_at[ask & (AHEAD - 1)][v][lane], ask0 + 16 * v);
+          copy16(slots_at[ask & (AHEAD - 1)][VECS + v][lane], ask1 + 16 * v);
+        }
+      }
+      ++ask;
+      ask_head += HPW;
+      ask0 += HPW * D * EIN;
+      ask1 += HPW * D * EIN;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");  // (an empty one keeps the count)
+  };
+#pragma unroll 1
+  for (int i = 0; i < AHEAD; ++i) request();
+  const auto arrived = [&](int s, float (&x)[8], float (&y)[8]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+    if constexpr (DIN == 0) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float4 f = *reinterpret_cast<const float4*>(slots_at[s & (AHEAD - 1)][v][lane]);
+        const float4 g = *reinterpret_cast<const float4*>(slots_at[s & (AHEAD - 1)][VECS + v][lane]);
+        x[4 * v] = f.x, x[4 * v + 1] = f.y, x[4 * v + 2] = f.z, x[4 * v + 3] = f.w;
+        y[4 * v] = g.x, y[4 * v + 1] = g.y, y[4 * v + 2] = g.z, y[4 * v + 3] = g.w;
+      }
+    } else {
+      load8<DIN>(slots_at[s & (AHEAD - 1)][0][lane], x);
+      load8<DIN>(slots_at[s & (AHEAD - 1)][1][lane], y);
+    }
+  };
+
+  // The TPH lanes of every head need the same 8 pairs' cosines and sines: each of the HPW groups of
+  // lanes works out 8 / HPW of them and the others take them over.
+  constexpr int MINE = 8 / HPW > 0 ? 8 / HPW : 1;
+  float cs[8], sn[8];
+  if (begin < sq + sk && a.rot > 0) {
+    const int64_t pos = a.positions[t];
+    float cm[MINE], sm[MINE];
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) {
+      const int i = (lane / TPH) * MINE + m;
+      const uint64_t phase = rotated ? a.phase[8 * p + i] : 0;
+      const uint32_t turn = static_cast<uint32_t>((static_cast<uint64_t>(pos) * phase) >> 32);
       const uint32_t quarter = (turn + 0x20000000u) >> 30;
       const int32_t rest = static_cast<int32_t>(turn - (quarter << 30));
       float s, c;
       sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s, &c);  // 2^-31: turns to half turns
       const float c1 = (quarter & 1u) ? s : c, s1 = (quarter & 1u) ? c : s;
-      cs[i] = (quarter == 1u || quarter == 2u) ? -c1 : c1;
-      sn[i] = (quarter >= 2u) ? -s1 : s1;
-      cs[i] *= a.rope_scale;
-      sn[i] *= a.rope_scale;
+      cm[m] = ((quarter == 1u || quarter == 2u) ? -c1 : c1) * a.rope_scale;
+      sm[m] = ((quarter >= 2u) ? -s1 : s1) * a.rope_scale;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = __shfl_sync(0xFFFFFFFFu, cm[i % MINE], (i / MINE) * TPH + p);
+      sn[i] = __shfl_sync(0xFFFFFFFFu, sm[i % MINE], (i / MINE) * TPH + p);
     }
   }
   int64_t row = t;
   bool put = true;
-  if (a.slots != nullptr && (a.Hkv > 0 || a.Hv > 0)) {
+  if (a.slots != nullptr && end > sq) {
     row = a.slots[t];
     put = row >= 0 && row < a.num_slots;
-    if (row >= a.num_slots && a.status != nullptr && lane == 0 && blockIdx.y == 0) set_status(a.status, FP2_DEV_SLOT_OOB);
+    if (row >= a.num_slots && a.status != nullptr && lane == 0 && end == sq + sk + sv)
+      set_status(a.status, FP2_DEV_SLOT_OOB);
   }
 
-  const int heads = a.Hq + a.Hkv + a.Hv;
-  const int h_begin = blockIdx.y * a.iters * HPW;
-  // Warp-uniform trip count: the shuffles of the norm need every lane.
-#pragma unroll 2
-  for (int it = 0; it < a.iters; ++it) {
-    const int h0 = h_begin + it * HPW;
-    if (h0 >= heads) break;
-    const int h = h0 + lane / TPH;
-    const int which = h < a.Hq ? 0 : (h < a.Hq + a.Hkv ? 1 : 2);
-    const int hh = which == 0 ? h : (which == 1 ? h - a.Hq : h - a.Hq - a.Hkv);
-    const bool live = h < heads && (which == 0 || put);
-    float x[8], y[8];
+#pragma unroll 1
+  for (int which = 0; which < 3; ++which) {
+    const int base = which == 0 ? 0 : (which == 1 ? sq : sq + sk), steps = which == 0 ? sq : (which == 1 ? sk : sv);
+    const int heads = which == 0 ? a.Hq : (which == 1 ? a.Hkv : a.Hv);
+    const int s0 = max(begin - base, 0), s1 = min(end - base, steps);
+    if (s0 >= s1 || (which > 0 && !put)) continue;  // (K and V without a place are the last steps)
+    char* dst = static_cast<char*>(which == 0 ? a.q_out : (which == 1 ? a.k_out : a.v_out)) +
+                (which == 0 ? t * a.q_out_stride : row * a.kv_out_stride) * EOUT;
+    const float inv = DOUT == 2 ? (which == 0 ? a.q_inv : (which == 1 ? a.k_inv : a.v_inv)) : 1.f;
+    if (which == 2) {
+      // V passes through: 16 neighbours a thread, whatever Q's layout.
+#pragma unroll 1
+      for (int s = s0; s < s1; ++s) {
+        const int h = s * HPW + lane / TPH;
+        float x[8], y[8];
+        arrived(base + s, x, y);
+        request();
+        if (DOUT == 2 && inv != 1.f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
-    if (live) {
-      const char* src = static_cast<const char*>(which == 0 ? a.q : (which == 1 ? a.k : a.v));
-      const int64_t stride = which == 0 ? a.q_stride : (which == 1 ? a.k_stride : a.v_stride);
-      src += (t * stride + static_cast<int64_t>(hh) * D) * EIN;
-      load8(src + e0 * EIN, DIN == 0, x);
-      load8(src + e1 * EIN, DIN == 0, y);
+          for (int i = 0; i < 8; ++i) x[i] *= inv, y[i] *= inv;
+        }
+        if (h < heads) {
+          char* to = dst + (static_cast<int64_t>(h) * D + 16 * p) * EOUT;
+          store8<DOUT>(to, x);
+          store8<DOUT>(to + 8 * EOUT, y);
+        }
+      }
+      continue;
     }
-    if (a.q_norm != nullptr || a.k_norm != nullptr) {
-      float ss = 0.f;
+    const void* w = which == 0 ? a.q_norm : a.k_norm;
+    const bool turns = rotated;
+    // Pair (x1, x2) becomes r (x1 f1 - x2 f2, x2 f3 + x1 f4); values that do not turn r (x f1), r (x f3).
+    float f1[8], f2[8], f3[8], f4[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
+    for (int i = 0; i < 8; ++i) f1[i] = f3[i] = 1.f, f2[i] = f4[i] = 0.f;
+    if (w != nullptr) {
+      load8<DIN>(static_cast<const char*>(w) + e0 * EIN, f1);
+      load8<DIN>(static_cast<const char*>(w) + e1 * EIN, f3);
+    }
+    if constexpr (INTER) {  // first and second values of the pairs from vectors of 8 neighbours each
+      float first[8], second[8];
 #pragma unroll
-      for (int o = 1; o < TPH; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      const void* w = which == 0 ? a.q_norm : (which == 1 ? a.k_norm : nullptr);
-      if (w != nullptr && live) {
-        const float r = rsqrtf(ss * (1.f / D) + a.norm_eps);
-        float w0[8], w1[8];
-        load8(static_cast<const char*>(w) + e0 * EIN, DIN == 0, w0);
-        load8(static_cast<const char*>(w) + e1 * EIN, DIN == 0, w1);
+      for (int i = 0; i < 4; ++i) {
+        first[i] = f1[2 * i], second[i] = f1[2 * i + 1];
+        first[4 + i] = f3[2 * i], second[4 + i] = f3[2 * i + 1];
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= r * w0[i], y[i] *= r * w1[i];
+      for (int i = 0; i < 8; ++i) f1[i] = first[i], f3[i] = second[i];
+    }
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w1 = f1[i], w2 = f3[i];
+        f1[i] = w1 * cs[i];
+        f2[i] = -(w2 * sn[i]);
+        f3[i] = w2 * cs[i];
+        f4[i] = w1 * sn[i];
       }
     }
-    if (rotated && which != 2) {
-      if (a.interleaved) {
+
+    __syncwarp();
+    float (*fac)[2][TPH][4] = factors[threadIdx.x >> 5];
+    if (lane < TPH) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x1 = x[2 * i], x2 = x[2 * i + 1], y1 = y[2 * i], y2 = y[2 * i + 1];
-          x[2 * i] = x1 * cs[i] - x2 * sn[i];
-          x[2 * i + 1] = x2 * cs[i] + x1 * sn[i];
-          y[2 * i] = y1 * cs[4 + i] - y2 * sn[4 + i];
-          y[2 * i + 1] = y2 * cs[4 + i] + y1 * sn[4 + i];
+      for (int q = 0; q < 2; ++q) {
+        *reinterpret_cast<float4*>(fac[0][q][p]) = make_float4(f1[4 * q], f1[4 * q + 1], f1[4 * q + 2], f1[4 * q + 3]);
+        *reinterpret_cast<float4*>(fac[1][q][p]) = make_float4(f2[4 * q], f2[4 * q + 1], f2[4 * q + 2], f2[4 * q + 3]);
+        *reinterpret_cast<float4*>(fac[2][q][p]) = make_float4(f3[4 * q], f3[4 * q + 1], f3[4 * q + 2], f3[4 * q + 3]);
+        *reinterpret_cast<float4*>(fac[3][q][p]) = make_float4(f4[4 * q], f4[4 * q + 1], f4[4 * q + 2], f4[4 * q + 3]);
+      }
+    }
+    __syncwarp();
+
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) {
+      const int h = s * HPW + lane / TPH;
+      float v0[8], v1[8], x1[8], x2[8];
+      arrived(base + s, v0, v1);
+      request();
+      float r = inv;
+      if (w != nullptr) {
+        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          ss = __ffma2_rn(make_float2(v0[i], v0[i + 1]), make_float2(v0[i], v0[i + 1]), ss);
+          ss = __ffma2_rn(make_float2(v1[i], v1[i + 1]), make_float2(v1[i], v1[i + 1]), ss);
         }
+        float sum = ss.x + ss.y;
+#pragma unroll
+        for (int o = 1; o < TPH; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        r *= rsqrtf(sum * (1.f / D) + a.norm_eps);
+      }
+      if constexpr (!INTER) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x1[i] = v0[i], x2[i] = v1[i];
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x1 = x[i], x2 = y[i];
-          x[i] = x1 * cs[i] - x2 * sn[i];
-          y[i] = x2 * cs[i] + x1 * sn[i];
+        for (int i = 0; i < 4; ++i) {
+          x1[i] = v0[2 * i], x2[i] = v0[2 * i + 1];
+          x1[4 + i] = v1[2 * i], x2[4 + i] = v1[2 * i + 1];
         }
       }
-    }
-    if (live) {
-      char* dst = static_cast<char*>(which == 0 ? a.q_out : (which == 1 ? a.k_out : a.v_out));
-      const int64_t at = which == 0 ? t * a.q_out_stride : row * a.kv_out_stride;
-      dst += (at + static_cast<int64_t>(hh) * D) * EOUT;
-      const float inv = which == 0 ? a.q_inv : (which == 1 ? a.k_inv : a.v_inv);
-      store8<DOUT>(dst + e0 * EOUT, x, inv);
-      store8<DOUT>(dst + e1 * EOUT, y, inv);
+      const float2 r2 = make_float2(r, r);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 g1 = *reinterpret_cast<const float4*>(fac[0][q][p]), g3 = *reinterpret_cast<const float4*>(fac[2][q][p]);
+        const float4 g2 = *reinterpret_cast<const float4*>(fac[1][q][p]), g4 = *reinterpret_cast<const float4*>(fac[3][q][p]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 4 * q + 2 * e;
+          const float2 a1 = make_float2(x1[i], x1[i + 1]), a2 = make_float2(x2[i], x2[i + 1]);
+          float2 y1 = __fmul2_rn(a1, e ? make_float2(g1.z, g1.w) : make_float2(g1.x, g1.y));
+          float2 y2 = __fmul2_rn(a2, e ? make_float2(g3.z, g3.w) : make_float2(g3.x, g3.y));
+          if (turns) {
+            y1 = __ffma2_rn(a2, e ? make_float2(g2.z, g2.w) : make_float2(g2.x, g2.y), y1);
+            y2 = __ffma2_rn(a1, e ? make_float2(g4.z, g4.w) : make_float2(g4.x, g4.y), y2);
+          }
+          y1 = __fmul2_rn(y1, r2);
+          y2 = __fmul2_rn(y2, r2);
+          x1[i] = y1.x, x1[i + 1] = y1.y;
+          x2[i] = y2.x, x2[i + 1] = y2.y;
+        }
+      }
+      if constexpr (!INTER) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v0[i] = x1[i], v1[i] = x2[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v0[2 * i] = x1[i], v0[2 * i + 1] = x2[i];
+          v1[2 * i] = x1[4 + i], v1[2 * i + 1] = x2[4 + i];
+        }
+      }
+      if (h < heads) {
+        char* at = dst + static_cast<int64_t>(h) * D * EOUT;
+        store8<DOUT>(at + e0 * EOUT, v0);
+        store8<DOUT>(at + e1 * EOUT, v1);
+      }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int DIN, int DOUT, int D>
 cudaError_t run_rotate(RotateArgs a, cudaStream_t stream) {
   constexpr int HPW = 32 / (D / 16);
-  const int heads = a.Hq + a.Hkv + a.Hv;
-  const int steps = (heads + HPW - 1) / HPW;
+  const int steps = (a.Hq + HPW - 1) / HPW + (a.Hkv + HPW - 1) / HPW + (a.Hv + HPW - 1) / HPW;
   // A warp walks all heads of its token when there are tokens enough to fill the GPU (148 SMs x 16
   // warps); below that the steps are spread over the grid's y, at the price of more sines.
   const int64_t want = (148 * 16 + a.tokens - 1) / a.tokens;
@@ -175,7 +343,8 @@ cudaError_t run_rotate(RotateArgs a, cudaStream_t stream) {
   a.iters = (steps + chunks - 1) / chunks;
   const dim3 grid(static_cast<unsigned>((a.tokens + kRotThreads / 32 - 1) / (kRotThreads / 32)),
                   (steps + a.iters - 1) / a.iters);
-  return launch_chained(rotate_kernel<DIN, DOUT, D>, grid, kRotThreads, 0, stream, 1, a);
+  return launch_chained(a.interleaved ? rotate_kernel<DIN, DOUT, D, true> : rotate_kernel<DIN, DOUT, D, false>, grid,
+                        kRotThreads, 0, stream, 1, a);
 }
 
 }  // namespace

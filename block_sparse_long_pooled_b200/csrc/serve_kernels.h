@@ -65,7 +65,7 @@ struct RotateArgs {
   int64_t num_slots;
   float q_inv, k_inv, v_inv;  // 1 / descale (E4M3 output)
   int64_t tokens;
-  int iters;             // heads per warp / heads per step of a warp
+  int iters;             // steps of a warp
   uint32_t* status;      // may be NULL
   uint64_t phase[64];    // turns per position of pair i, as a fraction of 2^64
 };
