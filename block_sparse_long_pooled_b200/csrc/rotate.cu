@@ -30,23 +30,25 @@ constexpr int kRotThreads = 128;
 #define MINB 7
 #endif
 
-// Eight values: four words of two bf16, or eight floats, from shared or global memory.
+// Eight values from four words of two bf16, or eight floats.
 template <int DIN>
-FP2_DEVICE void load8(const char* p, float (&x)[8]) {
-  const uint4 a = reinterpret_cast<const uint4*>(p)[0];
+FP2_DEVICE void unpack8(uint4 a, uint4 b, float (&x)[8]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   if constexpr (DIN == 0) {
-    const uint4 b = reinterpret_cast<const uint4*>(p)[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
   } else {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[2 * e] = __uint_as_float(w[e] << 16);
       x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
     }
   }
+}
+template <int DIN>
+FP2_DEVICE void load8(const char* p, float (&x)[8]) {
+  const uint4* v = reinterpret_cast<const uint4*>(p);
+  unpack8<DIN>(v[0], DIN == 0 ? v[1] : make_uint4(0, 0, 0, 0), x);
 }
 FP2_DEVICE uint32_t four_e4m3(float a, float b, float c, float d) {  // a in the lowest byte, saturating
   uint32_t r;
@@ -71,8 +73,20 @@ FP2_DEVICE void store8(char* p, const float (&x)[8]) {
   }
 }
 
-FP2_DEVICE void copy16(void* to, const char* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+FP2_DEVICE void copy16(uint32_t to, const char* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+FP2_DEVICE uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+FP2_DEVICE float4 lds_f4(uint32_t addr) {
+  const uint4 v = lds16(addr);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
 // DIN / DOUT: 0 f32, 1 bf16, 2 e4m3.
@@ -103,7 +117,9 @@ __global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kerne
   // registers, one step ahead, the loads left the SM waiting.  Every lane reads back what it copied.
   constexpr int AHEAD = 4, VECS = EIN / 2;             // 16-byte copies of a vector of 8
   __shared__ __align__(16) char ring[kRotThreads / 32][AHEAD][2 * VECS][32][16];
-  char(*const slots_at)[2 * VECS][32][16] = ring[threadIdx.x >> 5];
+  constexpr uint32_t VEC = 32 * 16, SLOT = 2 * VECS * VEC;
+  const uint32_t ring_at = smem_u32(ring[threadIdx.x >> 5][0][0][lane]);
+  uint32_t ask_slot = ring_at, get_slot = ring_at;
   // The next step to ask for: its section's end, this lane's head in it, and its two vectors.
   int ask = begin, ask_end = 0, ask_head = 0, ask_heads = 0;
   const char *ask0 = nullptr, *ask1 = nullptr;
@@ -125,11 +141,12 @@ __global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kerne
       if (ask_head < ask_heads) {
 #pragma unroll
         for (int v = 0; v < VECS; ++v) {
-          copy16(slots_at[ask & (AHEAD - 1)][v][lane], ask0 + 16 * v);
-          copy16(slots_at[ask & (AHEAD - 1)][VECS + v][lane], ask1 + 16 * v);
+          copy16(ask_slot + v * VEC, ask0 + 16 * v);
+          copy16(ask_slot + (VECS + v) * VEC, ask1 + 16 * v);
         }
       }
       ++ask;
+      ask_slot = ask_slot == ring_at + (AHEAD - 1) * SLOT ? ring_at : ask_slot + SLOT;
       ask_head += HPW;
       ask0 += HPW * D * EIN;
       ask1 += HPW * D * EIN;
@@ -138,20 +155,12 @@ __global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kerne
   };
 #pragma unroll 1
   for (int i = 0; i < AHEAD; ++i) request();
-  const auto arrived = [&](int s, float (&x)[8], float (&y)[8]) {
+  const auto arrived = [&](float (&x)[8], float (&y)[8]) {
     asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
-    if constexpr (DIN == 0) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const float4 f = *reinterpret_cast<const float4*>(slots_at[s & (AHEAD - 1)][v][lane]);
-        const float4 g = *reinterpret_cast<const float4*>(slots_at[s & (AHEAD - 1)][VECS + v][lane]);
-        x[4 * v] = f.x, x[4 * v + 1] = f.y, x[4 * v + 2] = f.z, x[4 * v + 3] = f.w;
-        y[4 * v] = g.x, y[4 * v + 1] = g.y, y[4 * v + 2] = g.z, y[4 * v + 3] = g.w;
-      }
-    } else {
-      load8<DIN>(slots_at[s & (AHEAD - 1)][0][lane], x);
-      load8<DIN>(slots_at[s & (AHEAD - 1)][1][lane], y);
-    }
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    unpack8<DIN>(lds16(get_slot), DIN == 0 ? lds16(get_slot + VEC) : zero, x);
+    unpack8<DIN>(lds16(get_slot + VECS * VEC), DIN == 0 ? lds16(get_slot + 3 * VEC) : zero, y);
+    get_slot = get_slot == ring_at + (AHEAD - 1) * SLOT ? ring_at : get_slot + SLOT;
   };
 
   // The TPH lanes of every head need the same 8 pairs' cosines and sines: each of the HPW groups of
@@ -200,21 +209,23 @@ __global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kerne
     const float inv = DOUT == 2 ? (which == 0 ? a.q_inv : (which == 1 ? a.k_inv : a.v_inv)) : 1.f;
     if (which == 2) {
       // V passes through: 16 neighbours a thread, whatever Q's layout.
+      int h = s0 * HPW + lane / TPH;
+      char* to = dst + (static_cast<int64_t>(h) * D + 16 * p) * EOUT;
 #pragma unroll 1
       for (int s = s0; s < s1; ++s) {
-        const int h = s * HPW + lane / TPH;
         float x[8], y[8];
-        arrived(base + s, x, y);
+        arrived(x, y);
         request();
         if (DOUT == 2 && inv != 1.f) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] *= inv, y[i] *= inv;
         }
         if (h < heads) {
-          char* to = dst + (static_cast<int64_t>(h) * D + 16 * p) * EOUT;
           store8<DOUT>(to, x);
           store8<DOUT>(to + 8 * EOUT, y);
         }
+        to += HPW * D * EOUT;
+        h += HPW;
       }
       continue;
     }
@@ -262,11 +273,14 @@ __global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kerne
     }
     __syncwarp();
 
+    int h = s0 * HPW + lane / TPH;
+    char* to = dst + (static_cast<int64_t>(h) * D + e0) * EOUT;
+    const int apart = (e1 - e0) * EOUT;
+    const uint32_t fac_at = smem_u32(fac[0][0][p]);
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-      const int h = s * HPW + lane / TPH;
       float v0[8], v1[8], x1[8], x2[8];
-      arrived(base + s, v0, v1);
+      arrived(v0, v1);
       request();
       float r = inv;
       if (w != nullptr) {
@@ -294,8 +308,8 @@ __global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kerne
       const float2 r2 = make_float2(r, r);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float4 g1 = *reinterpret_cast<const float4*>(fac[0][q][p]), g3 = *reinterpret_cast<const float4*>(fac[2][q][p]);
-        const float4 g2 = *reinterpret_cast<const float4*>(fac[1][q][p]), g4 = *reinterpret_cast<const float4*>(fac[3][q][p]);
+        const float4 g1 = lds_f4(fac_at + q * (TPH * 16)), g3 = lds_f4(fac_at + (4 + q) * (TPH * 16));
+        const float4 g2 = lds_f4(fac_at + (2 + q) * (TPH * 16)), g4 = lds_f4(fac_at + (6 + q) * (TPH * 16));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = 4 * q + 2 * e;
@@ -323,10 +337,11 @@ __global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kerne
         }
       }
       if (h < heads) {
-        char* at = dst + static_cast<int64_t>(h) * D * EOUT;
-        store8<DOUT>(at + e0 * EOUT, v0);
-        store8<DOUT>(at + e1 * EOUT, v1);
+        store8<DOUT>(to, v0);
+        store8<DOUT>(to + apart, v1);
       }
+      to += HPW * D * EOUT;
+      h += HPW;
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
