@@ -440,40 +440,51 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[s
 
 
 class _Handle:
-    """A C struct, the tensors it points into (kept alive here) and the device they are on."""
+    """A C struct, the tensors it points into (kept alive here) and the device they are on.  The calls on
+    it last microseconds, so what they need of torch and of the library is looked up once."""
 
     def __init__(self, struct, tensors, arrays=()):
+        import torch
         self.struct, self.ref = struct, ctypes.byref(struct)
         self.keep = (tuple(tensors), tuple(arrays))
         devices = {t.device for t in tensors if t is not None}
         if len(devices) > 1:
             raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
-        device = devices.pop()
-        self.device = device
-        self.index = device.index if device.type == "cuda" else None
+        self.device = devices.pop()
+        self.cuda = self.device.type == "cuda"
+        self.index = self.device.index if self.cuda else -1
+        self.lib = load_library()
+        if self.cuda:
+            # current_stream(device).cuda_stream and current_device() without the objects around them
+            self.raw_stream, self.current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            self.guard, self.alone = torch.cuda.device, torch.cuda.device_count() == 1
 
-    def call(self, name: str, *args, stream=None):
-        """The C entry point on this handle, on its device and (stream None) that device's current stream."""
-        import torch
-        fn = getattr(load_library(), name)
-        if self.index is None:
-            return _check(fn(self.ref, *args, 0 if stream is None else _stream_handle(stream)))
-        if stream is None:
-            raw = torch._C._cuda_getCurrentRawStream(self.index)   # current_stream(...).cuda_stream, without the object
+    def call(self, fn, args, stream):
+        """The C entry point fn on this handle, on its device and (stream None) that device's current stream."""
+        if not self.cuda:
+            status = fn(self.ref, *args, 0 if stream is None else _stream_handle(stream))
         else:
-            raw = _stream_handle(stream)
-        if torch._C._cuda_getDevice() == self.index:
-            return _check(fn(self.ref, *args, raw))
-        with torch.cuda.device(self.index):
-            return _check(fn(self.ref, *args, raw))
+            raw = self.raw_stream(self.index) if stream is None else _stream_handle(stream)
+            if self.alone or self.current() == self.index:
+                status = fn(self.ref, *args, raw)
+            else:
+                with self.guard(self.index):
+                    status = fn(self.ref, *args, raw)
+        if status:
+            _check(status)
 
     def pointer(self, t, dtype, shape, what: str):
         """data_ptr of a contiguous tensor of this handle's device, or None."""
         if t is None:
             return None
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != self.device:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self.index:
             raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}")
         return t.data_ptr()
+
+    def space(self, scratch):
+        if scratch.get_device() != self.index:
+            raise ValueError(f"scratch must be on {self.device}")
+        return scratch.data_ptr(), scratch.nbytes
 
 
 class Rotation(_Handle):
@@ -481,7 +492,13 @@ class Rotation(_Handle):
 
 
 class Decode(_Handle):
-    pass
+    def __init__(self, struct, tensors, arrays=()):
+        import torch
+        super().__init__(struct, tensors, arrays)
+        tokens, heads, dim = tensors[0].shape
+        self.out_shape, self.lse_shape = (tokens, heads, dim), (heads, tokens)
+        self.seqs, self.kv_heads, self.has_v = struct.num_seqs, struct.cache.num_kv_heads, bool(struct.cache.v)
+        self.types = torch.bfloat16, torch.float32, torch.int32
 
 
 class Eviction(_Handle):
@@ -621,7 +638,7 @@ def make_rotate(q, k, v, positions, rope: Optional[Rope], q_out, k_out, v_out, s
 def fp2_rotate(rotation: Rotation, status_dev=None, stream=None):
     """Head norms, rotary positions and cache append (include/fp2.h).  status_dev: optional int32/uint32
     device word that FP2_DEV_* bits are OR-ed into."""
-    rotation.call("fp2_rotate", _ptr(status_dev), stream=stream)
+    rotation.call(rotation.lib.fp2_rotate, (None if status_dev is None else status_dev.data_ptr(),), stream)
 
 
 def make_decode(q, cache: Cache, cu_seqlens, kv_len, max_kv_len: int, num_kv_heads: Optional[int] = None,
@@ -663,28 +680,25 @@ def fp2_decode_workspace(decode: Decode) -> int:
 
 def fp2_tree_attend(decode: Decode, out, lse, scratch, stream=None):
     """Attention of the new tokens over their caches.  out [T, Hq, d] bf16; lse [Hq, T] f32 or None."""
-    import torch
-    s = decode.struct
-    T, hq, d = decode.keep[0][0].shape
-    if s.cache.v is None:
+    if not decode.has_v:
         raise ValueError("the cache has no v")
-    decode.call("fp2_tree_attend", decode.pointer(out, torch.bfloat16, (T, hq, d), "out"),
-                decode.pointer(lse, torch.float32, (hq, T), "lse"), scratch.data_ptr(), scratch.nbytes, stream=stream)
+    bf16, f32, _ = decode.types
+    decode.call(decode.lib.fp2_tree_attend, (decode.pointer(out, bf16, decode.out_shape, "out"),
+                                             decode.pointer(lse, f32, decode.lse_shape, "lse"),
+                                             *decode.space(scratch)), stream)
 
 
 def fp2_key_mass(decode: Decode, lse, mass_in, mass_out, scratch, decay: float = 1.0, mass_len=None, stream=None):
     """mass_out = decay * mass_in + the attention weight that each key receives from the new tokens.
     lse [Hq, T] from fp2_tree_attend; mass_in (or None: zero), mass_out [num_seqs, Hkv, >= max_kv_len]
     f32 (they may be one tensor); mass_len [num_seqs] int32: keys that mass_in covers, or None: all."""
-    import torch
-    s = decode.struct
-    shape = (s.num_seqs, s.cache.num_kv_heads, mass_out.shape[-1])
-    T, hq, _ = decode.keep[0][0].shape
-    decode.call("fp2_key_mass", decode.pointer(lse, torch.float32, (hq, T), "lse"),
-                decode.pointer(mass_in, torch.float32, shape, "mass_in"),
-                decode.pointer(mass_out, torch.float32, shape, "mass_out"), shape[2],
-                decode.pointer(mass_len, torch.int32, (s.num_seqs,), "mass_len"), decay, scratch.data_ptr(),
-                scratch.nbytes, stream=stream)
+    _, f32, i32 = decode.types
+    shape = (decode.seqs, decode.kv_heads, mass_out.shape[-1])
+    decode.call(decode.lib.fp2_key_mass, (decode.pointer(lse, f32, decode.lse_shape, "lse"),
+                                          decode.pointer(mass_in, f32, shape, "mass_in"),
+                                          decode.pointer(mass_out, f32, shape, "mass_out"), shape[2],
+                                          decode.pointer(mass_len, i32, (decode.seqs,), "mass_len"), decay,
+                                          *decode.space(scratch)), stream)
 
 
 def make_evict(cache: Cache, kv_len, max_kv_len: int, mass, budget: int, sink: int, window: int, cache_out: Cache,
@@ -717,4 +731,4 @@ def fp2_evict_workspace(eviction: Eviction) -> int:
 
 def fp2_evict(eviction: Eviction, scratch, stream=None):
     """Keep each (sequence, KV head)'s heaviest keys, in another cache (include/fp2.h)."""
-    eviction.call("fp2_evict", scratch.data_ptr(), scratch.nbytes, stream=stream)
+    eviction.call(eviction.lib.fp2_evict, eviction.space(scratch), stream)
