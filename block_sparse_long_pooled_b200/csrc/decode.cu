@@ -140,7 +140,7 @@ struct Tree {
   static constexpr int STAGE_BYTES = 2 * KV_BYTES;
   static constexpr int Q_BYTES = ROWS * D * 2;
   static constexpr int OS = D + 8;                              // row stride of the joined output, floats
-  static constexpr int O_BYTES = ROWS * OS * 4;
+  static constexpr int O_BYTES = WN * ROWS * OS * 4;            // of every key warp
   static constexpr int FIXED = 1024 /* alignment */ + Q_BYTES + O_BYTES + WN * ROWS * 8 + (FP2_MAX_SEQS + 1) * 8 +
                                FP2_MAX_SEQS * 4 + 256;
   static constexpr int CTAS = ROWS <= 32 ? 2 : 1;               // per SM
@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
       if (++s == C::STAGES) s = 0;
     }
 
-    // Join the four key warps of each row: agree on the maximum, then add O up in warp order.
+    // The four key warps lay down what they have of each row; whoever writes the row adds it up.  (Adding
+    // it up in shared memory warp by warp cost four barriers more, 0.6 us of a decode step's 6.)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -467,56 +468,23 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
         float x = sum[m][i];
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-        if ((lane & 3) == 0)
-          ml_smem[wn * C::ROWS + (wm * MT + m) * 16 + (lane >> 2) + 8 * i] = make_float2(mx[m][i], x);
+        const int row = (wm * MT + m) * 16 + (lane >> 2) + 8 * i;
+        if ((lane & 3) == 0) ml_smem[wn * C::ROWS + row] = make_float2(mx[m][i], x);
+        if (row0 + row >= rows) continue;
+        float* dst = o_smem + (wn * C::ROWS + row) * C::OS;
+        if constexpr (!C::F16) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2*>(dst + 8 * n + 2 * (lane & 3)) = make_float2(o[m][n][2 * i], o[m][n][2 * i + 1]);
+        } else {
+          // columns 2q, 2q+1 of the even and odd accumulators are d = 4q, 4q+2 and 4q+1, 4q+3
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n)
+            *reinterpret_cast<float4*>(dst + 16 * n + 4 * (lane & 3)) =
+                make_float4(o[m][2 * n][2 * i], o[m][2 * n + 1][2 * i], o[m][2 * n][2 * i + 1], o[m][2 * n + 1][2 * i + 1]);
+        }
       }
     consumer_sync<C::CONSUMERS>();
-    float fac[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = (wm * MT + m) * 16 + (lane >> 2) + 8 * i;
-        float top = neg_inf();
-#pragma unroll
-        for (int w = 0; w < C::WN; ++w) top = fmaxf(top, ml_smem[w * C::ROWS + row].x);
-        fac[m][i] = mx[m][i] == neg_inf() ? 0.f : fast_exp2((mx[m][i] - top) * a.scale_log2);
-      }
-    for (int w = 0; w < C::WN; ++w) {
-      if (w == wn) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float* dst = o_smem + ((wm * MT + m) * 16 + (lane >> 2) + 8 * i) * C::OS;
-            const float f = fac[m][i];
-            if constexpr (!C::F16) {
-#pragma unroll
-              for (int n = 0; n < D / 8; ++n) {
-                float2* at = reinterpret_cast<float2*>(dst + 8 * n + 2 * (lane & 3));
-                float2 old = w == 0 ? make_float2(0.f, 0.f) : *at;
-                // a row this warp saw nothing of adds nothing (its accumulators are zero)
-                old.x += o[m][n][2 * i] * f;
-                old.y += o[m][n][2 * i + 1] * f;
-                *at = old;
-              }
-            } else {
-              // columns 2q, 2q+1 of the even and odd accumulators are d = 4q, 4q+2 and 4q+1, 4q+3
-#pragma unroll
-              for (int n = 0; n < D / 16; ++n) {
-                float4* at = reinterpret_cast<float4*>(dst + 16 * n + 4 * (lane & 3));
-                float4 old = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *at;
-                old.x += o[m][2 * n][2 * i] * f;
-                old.y += o[m][2 * n + 1][2 * i] * f;
-                old.z += o[m][2 * n][2 * i + 1] * f;
-                old.w += o[m][2 * n + 1][2 * i + 1] * f;
-                *at = old;
-              }
-            }
-          }
-      }
-      consumer_sync<C::CONSUMERS>();
-    }
 
     // Out: the whole item, or this group's part of it.
     const bool whole = p.t0 == 0 && p.t1 == p.tiles;
@@ -526,15 +494,22 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
       const int rr = i / LANES, c = (i - rr * LANES) * 4, m = row0 + rr;
       if (m >= rows) continue;
       float top = neg_inf(), total = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < C::WN; ++w) top = fmaxf(top, ml_smem[w * C::ROWS + rr].x);
 #pragma unroll
       for (int w = 0; w < C::WN; ++w) {
         const float2 x = ml_smem[w * C::ROWS + rr];
         // a warp that saw nothing has the sum 0; one whose scores are all NaN has the maximum -inf too
-        total += x.y == 0.f ? 0.f : x.y * fast_exp2((x.x - top) * a.scale_log2);
+        if (x.y == 0.f) continue;
+        const float f = fast_exp2((x.x - top) * a.scale_log2);
+        const float4 part = *reinterpret_cast<const float4*>(o_smem + (w * C::ROWS + rr) * C::OS + c);
+        total += x.y * f;
+        v.x += part.x * f;
+        v.y += part.y * f;
+        v.z += part.z * f;
+        v.w += part.w * f;
       }
-      const float4 v = *reinterpret_cast<const float4*>(o_smem + rr * C::OS + c);
       if (whole) {
         const int tok = m / a.G, h = g * a.G + (m - tok * a.G);
         const float f = total == 0.f ? 0.f : a.v_descale / total;
@@ -558,10 +533,7 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
     if (g == 0 && tid == 0 && u >= u1) {
       int4 d = make_int4(-1, 0, 0, 0);
       if (p.t0 == 0 && p.t1 < p.tiles) {
-        const long long last = u1 + (p.tiles - p.t1) - 1;  // the item's last unit
-        int e = grp + 1;
-        while (units * (e + 1) / ng <= last) ++e;
-        d = make_int4(nth == 0 ? 0 : 1, p.r, p.rt, e - grp + 1);
+        d = make_int4(nth == 0 ? 0 : 1, p.r, p.rt, group_of(units, ng, u1 + (p.tiles - p.t1) - 1) - grp + 1);
       }
       a.desc[grp] = d;
     }
@@ -586,39 +558,59 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     const int64_t slot = (static_cast<int64_t>(grp + i) * a.Hkv + g) * 2 + (i == 0 ? d.x : 0);
     return slot * a.part_rows + rr;
   };
-  float top = neg_inf();
-  bool any = false;  // some piece saw a key (all of whose scores may be NaN)
-  for (int i = lane; i < d.w; i += 32) {
-    const float2 ml = a.part_ml[at(i)];
-    top = fmaxf(top, ml.x);
-    any |= !(ml.y == 0.f);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   constexpr int V = D / 32;
-  float acc[V], total = 0.f;
+  float acc[V], total = 0.f, top = neg_inf();
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  if (__any_sync(0xFFFFFFFFu, any)) {
-#pragma unroll 8
-    for (int i = 0; i < d.w; ++i) {  // no branch: the loads of eight pieces are in flight at once
-      const int64_t row = at(i);
-      const float2 ml = a.part_ml[row];
-      const float* src = a.part_o + row * D + lane * V;
-      float x[V];
-      if constexpr (V == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        x[0] = v.x, x[1] = v.y;
-      }
-      // a piece that saw nothing of the row may not even have written its part_o
-      const bool saw = !(ml.y == 0.f);
-      const float w = saw ? fast_exp2(ml.x - top) : 0.f;
-      total += saw ? w * ml.y : 0.f;
+  // Up to 32 pieces at a time, lane i with the statistics of piece i; all their rows are on their way
+  // together, 16 at a time.
+  for (int i0 = 0; i0 < d.w; i0 += 32) {
+    const int n = min(32, d.w - i0);
+    const float2 ml = lane < n ? a.part_ml[at(i0 + lane)] : make_float2(neg_inf(), 0.f);
+    float x[16][V];
+    const auto fetch = [&](int i1) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += saw ? w * x[e] : 0.f;
+      for (int i = 0; i < 16; ++i) {
+        if (i1 + i >= n) break;
+        const float* src = a.part_o + at(i0 + i1 + i) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          x[i][0] = v.x, x[i][1] = v.y;
+        }
+      }
+    };
+    fetch(0);
+    float now = ml.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, o));
+    now = fmaxf(now, top);
+    // what came before, if anything did (a piece whose scores were all NaN has a sum but no maximum)
+    const float f = total == 0.f ? 0.f : fast_exp2(top - now);
+    total = total == 0.f ? 0.f : total * f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = total == 0.f ? 0.f : acc[e] * f;
+    top = now;
+    // a piece that saw nothing of the row has the sum 0 and may not even have written its part_o
+    const bool saw = !(ml.y == 0.f);
+    const float w = saw ? fast_exp2(ml.x - top) : 0.f;
+    float sum = saw ? w * ml.y : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    total += sum;
+    const uint32_t seen = __ballot_sync(0xFFFFFFFFu, saw);
+    for (int i1 = 0; i1 < n; i1 += 16) {
+      if (i1 > 0) fetch(i1);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i1 + i >= n) break;
+        const float wi = __shfl_sync(0xFFFFFFFFu, w, i1 + i);
+        const bool use = (seen >> (i1 + i)) & 1u;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += use ? wi * x[i][e] : 0.f;
+      }
     }
   }
   const int tok = m / a.G, h = g * a.G + (m - tok * a.G);

@@ -74,6 +74,11 @@ FP2_DEVICE int active_groups(long long units, int groups) {
   return static_cast<int>(units < 1 ? 1 : (units < groups ? units : groups));
 }
 
+// The group that works on unit u: shares begin at units * group / groups.
+FP2_DEVICE int group_of(long long units, int groups, long long u) {
+  return static_cast<int>(((u + 1) * groups - 1) / units);
+}
+
 // The CTA's status bits go to a word of its own in scratch (see serve_kernels.h); every thread
 // calls it, with nothing of the CTA's left to do.
 FP2_DEVICE void store_status(const DecodeArgs& a, const uint32_t* status) {

@@ -730,10 +730,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (g == 0 && tid == 0 && u >= u1) {
         int4 d = make_int4(-1, 0, 0, 0);
         if (p.t0 == 0 && p.t1 < p.tiles) {
-          const long long last = u1 + (p.w * p.tiles - p.end) - 1;  // the item's last unit
-          int e = grp + 1;
-          while (units * (e + 1) / ng <= last) ++e;
-          d = make_int4(nth == 0 ? 0 : 1, p.r, p.rt, e - grp + 1);
+          d = make_int4(nth == 0 ? 0 : 1, p.r, p.rt, group_of(units, ng, u1 + (p.w * p.tiles - p.end) - 1) - grp + 1);
         }
         a.desc[grp] = d;
       }
