@@ -16,8 +16,8 @@
 // (Adding the histograms up in rank 0 cost 6 us a digit for 16 ranks, one warp reading all ranks 5.)
 // Weights of zero, in earnest the most frequent one, are counted by ballot: one shared-memory add a
 // warp instead of one a key on the same word.  Up to 16 keys a thread stay in registers in between (8,192 a rank); longer ranges are
-// read again from L2.  Ballots in index order then give every kept key its row; ranks know the counts
-// of the ranks before them, so nothing depends on timing.  After that the rows are moved, each rank an
+// read again from L2.  Ballots in index order then give every kept key its row: what the ranks before
+// keep follows from their histograms, so nothing depends on timing.  After that the rows are moved, each rank an
 // equal share of the output rows whatever range they came from: the addresses of 512 rows at a time are
 // looked up first, so that the copies themselves wait only for their data.
 #include <cooperative_groups.h>
@@ -49,7 +49,6 @@ struct EvictShared {
   uint32_t groups[3][kGroups];
   uint32_t got[kMaxRanks][kGroups];  // groups, then bins, of every rank
   uint32_t got_bins[kMaxRanks][32];
-  uint32_t count[2];          // of this rank: keys kept outright, keys equal to the threshold
   uint32_t warp_sel[kWarps], warp_eq[kWarps];
   int64_t from[kChunk], to[kChunk];
   uint32_t status;
@@ -132,6 +131,9 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     for (int i = tid; i < 3 * kBins; i += kThreads) (&s.bins[0][0])[i] = 0;
     uint32_t need = static_cast<uint32_t>(a.budget - a.sink - a.window);  // of the competing keys
     uint32_t prefix = 0, mask = 0;
+    // What the ranks before this one keep: first of the keys that do not compete.
+    const int low_keys = min(first * 32, n);
+    uint32_t sel_before = static_cast<uint32_t>(min(low_keys, free0) + max(low_keys - free1, 0)), eq_before = 0;
     __syncthreads();
     // need == 0: no competing key stays, and no key's order value exceeds this threshold.
     bool done = need == 0;
@@ -180,12 +182,14 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
         *reinterpret_cast<uint2*>(&s.got[warp][2 * lane]) =
             *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s.groups[pass][2 * lane], warp));
       if (ranks > 1) __syncthreads();
-      uint32_t g0 = 0, g1 = 0;
+      uint32_t g0 = 0, g1 = 0, low0 = 0, low1 = 0;  // low: of the ranks before this one
+#pragma unroll 4
       for (int q = 0; q < ranks; ++q) {
         const uint2 x = *reinterpret_cast<const uint2*>(ranks > 1 ? &s.got[q][kGroups - 2 - 2 * lane]
                                                                   : &s.groups[pass][kGroups - 2 - 2 * lane]);
         g0 += x.y;
         g1 += x.x;
+        if (q == rank - 1) low0 = g0, low1 = g1;
       }
       uint32_t above = before(g0 + g1);
       // The one group, then the one bin, in which the need-th key lies (need is at most all of them).
@@ -197,10 +201,19 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
         if (warp < ranks) s.got_bins[warp][lane] = *cluster.map_shared_rank(&mine[group * 32 + lane], warp);
         __syncthreads();
       }
-      uint32_t x = 0;
-      for (int q = 0; q < ranks; ++q) x += ranks > 1 ? s.got_bins[q][31 - lane] : mine[group * 32 + 31 - lane];
+      uint32_t x = 0, low = 0;
+#pragma unroll 4
+      for (int q = 0; q < ranks; ++q) {
+        x += ranks > 1 ? s.got_bins[q][31 - lane] : mine[group * 32 + 31 - lane];
+        if (q == rank - 1) low = x;
+      }
       above = before(x);
       const int at = __ffs(__ballot_sync(0xFFFFFFFFu, above < left && above + x >= left)) - 1;
+      // Keys of the ranks before this one: above the bin (they stay), and in it.
+      const int first_group = kGroups - 1 - 2 * lane;
+      sel_before += __reduce_add_sync(0xFFFFFFFFu, (first_group > group ? low0 : 0u) + (first_group - 1 > group ? low1 : 0u) +
+                                                       (lane < at ? low : 0u));
+      eq_before = __shfl_sync(0xFFFFFFFFu, low, at);
       prefix |= static_cast<uint32_t>(group * 32 + 31 - at) << shift;
       mask |= digit << shift;
       need = left - __shfl_sync(0xFFFFFFFFu, above, at);
@@ -209,6 +222,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
         prefix -= 1;
         need = 0;
         done = true;
+        sel_before += eq_before;
+        eq_before = 0;
       }
     }
     // Keys above `prefix` stay, and of those equal to it the first `need`.
@@ -236,33 +251,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
       s.warp_eq[warp] = eq;
     }
     __syncthreads();
-    uint32_t sel_before = lane < warp ? s.warp_sel[lane & (kWarps - 1)] : 0u;
-    uint32_t eq_before = lane < warp ? s.warp_eq[lane & (kWarps - 1)] : 0u;
-    if (ranks > 1) {
-      if (warp == 0) {
-        uint32_t x = lane < kWarps ? s.warp_sel[lane] : 0u, y = lane < kWarps ? s.warp_eq[lane] : 0u;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-          y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
-        }
-        if (lane == 0) {
-          s.count[0] = x;
-          s.count[1] = y;
-        }
-      }
-      cluster.sync();
-      if (lane < rank) {  // (up to 16 ranks)
-        const uint32_t* c = cluster.map_shared_rank(&s.count[0], lane);
-        sel_before += c[0];
-        eq_before += c[1];
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      sel_before += __shfl_xor_sync(0xFFFFFFFFu, sel_before, o);
-      eq_before += __shfl_xor_sync(0xFFFFFFFFu, eq_before, o);
-    }
+    sel_before += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s.warp_sel[lane & (kWarps - 1)] : 0u);
+    eq_before += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s.warp_eq[lane & (kWarps - 1)] : 0u);
     const uint32_t below = (1u << lane) - 1;
 #pragma unroll 1
     for (int t0 = w0; t0 < w1; t0 += kHeld) {
