@@ -112,7 +112,7 @@ fp2_status check_rotation(const fp2_rotation* p) {
   if (p->rotary_dim > 0) {
     if (p->inv_freq_host == nullptr) return invalid("inv_freq_host is NULL");
     for (int i = 0; i < p->rotary_dim / 2; ++i)
-      if (!std::isfinite(p->inv_freq_host[i])) return invalid("inv_freq must be finite");
+      if (!(std::fabs(p->inv_freq_host[i]) < 1e18)) return invalid("inv_freq must be finite (and below 1e18)");
   }
   if (p->tokens == 0) return FP2_OK;
   if (p->rotary_dim > 0 && (p->positions == nullptr || !aligned4(p->positions)))
@@ -171,14 +171,12 @@ fp2_status run_rotate(const fp2_rotation* p, uint32_t* status_dev, cudaStream_t 
   a.v_inv = 1.f / p->v_descale;
   a.tokens = p->tokens;
   a.status = status_dev;
-  // Turns per position as a fraction of 2^64 (rotate.cu): whole turns drop out.
-  constexpr long double kTwoPi = 6.283185307179586476925286766559005768L;
+  // Turns per position as a fraction of 2^64 (rotate.cu): whole turns drop out (frequencies below 2^60).
+  constexpr long double kTurn = 0.15915494309189533576888376337251436203L;  // 1 / 2 pi
   for (int i = 0; i < p->rotary_dim / 2; ++i) {
-    long double turns = static_cast<long double>(p->inv_freq_host[i]) / kTwoPi;
-    turns -= std::floor(turns);
-    long double scaled = turns * 18446744073709551616.0L;
-    if (scaled >= 18446744073709551615.0L) scaled = 0.0L;
-    a.phase[i] = static_cast<uint64_t>(scaled);
+    const long double turns = static_cast<long double>(p->inv_freq_host[i]) * kTurn;
+    const long double part = turns - static_cast<long double>(static_cast<int64_t>(turns));  // in (-1, 1)
+    a.phase[i] = static_cast<uint64_t>(static_cast<int64_t>(part * 9223372036854775808.0L)) << 1;
   }
   return launched(fp2::launch_rotate(p->in_dtype, p->out_dtype, p->head_dim, a, st));
 }
