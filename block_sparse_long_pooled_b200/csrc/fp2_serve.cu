@@ -440,6 +440,7 @@ fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void
   a.part_ml = reinterpret_cast<float2*>(base + c.off_ml);
   a.part_o = reinterpret_cast<float*>(base + c.off_o);
   a.part_rows = c.part_rows;
+  a.max_rows = c.max_rows;
   a.v_ptr = decode->cache.v;
   a.kv_stride = decode->cache.stride_tok;
   a.kv_stride_outer = decode->cache.stride_outer;

@@ -103,7 +103,8 @@ struct DecodeArgs {
   int4* desc;                 // [groups] {slot of the first piece of a split item or -1, sequence, row tile, pieces}
   float2* part_ml;            // [groups * Hkv * 2][rows] running maximum (log2 units) and sum
   float* part_o;              // [groups * Hkv * 2][part_rows][d]
-  int part_rows;              // rows of a partial result: of an item
+  int part_rows;              // rows of a partial result
+  int max_rows;               // most query rows per (sequence, KV head)
   const void* v_ptr;          // V once more, in elements, for values that the products leave out
   int64_t kv_stride, kv_stride_outer;
   // key mass

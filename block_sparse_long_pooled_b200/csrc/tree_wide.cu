@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t tmem = tmem_slot;
   scan_units<C::TILE>(a, P, 128, 0, pre, len, &status_word);
   const long long units = pre[P.num_seqs];
-  const int ng = active_groups(units, a.groups);
+  // Partial results of 256 rows cost as much as four units: fewer CTAs then.
+  const int ng = active_groups(a.max_rows > 128 ? (units + 3) / 4 : units, a.groups);
   const bool idle = grp >= ng;
   const long long u0 = idle ? 0 : units * grp / ng, u1 = idle ? 0 : units * (grp + 1) / ng;
   if (idle && g == 0 && tid == 0) a.desc[grp] = make_int4(-1, 0, 0, 0);
@@ -515,19 +516,32 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const bool busy = __any_sync(0xFFFFFFFFu, mine);
       const int n = p.t1 - p.t0;
 
-      // Q: each row by the thread that owns it (parity: by stream 0's).  The row before has been
-      // used: this thread has seen the last product of the piece before.
+      // Q: the warp's 32 rows, RPL of them at a time with their chunks side by side in the lanes, every load
+      // on its way at once (parity: by stream 0).  The rows before have been used: this warp has seen the
+      // last product of the piece before.
       if (pair || s == 0) {
+        constexpr int CH = D * C::ELT / 16, RPL = 32 / CH;
         const uint32_t q_at = sbase + C::OFF_Q + (pair ? s : 0) * C::Q_BYTES;
-        const int from = p.rt * 256 + (pair ? local : (shift ? rt & 63 : rt));
-        const bool there = from < rows;
-        const int ft = there ? from / a.G : 0, fh = g * a.G + (there ? from - ft * a.G : 0);
+        const int ch = lane % CH, r0 = (warp & 3) * 32 + lane / CH;  // this lane's chunk and first row
+        const int from0 = p.rt * 256 + (pair ? s * 128 : 0) + (shift ? r0 & 63 : r0);
+        int ft = from0 / a.G, fh = from0 - ft * a.G;                 // token and head go along by steps of RPL rows
+        const int step_t = RPL / a.G, step_h = RPL - step_t * a.G;
         const char* src = static_cast<const char*>(a.q) +
-                          ((static_cast<int64_t>(tok0) + ft) * a.q_stride + static_cast<int64_t>(fh) * D) * C::ELT;
-#pragma unroll 8
-        for (int c = 0; c < D * C::ELT / 16; ++c)
-          sts16(q_at + box_addr<128>(rt, c),
-                there ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0));
+                          (static_cast<int64_t>(tok0) * a.q_stride + static_cast<int64_t>(g) * a.G * D) * C::ELT + 16 * ch;
+        uint4 v[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (from0 + i * RPL < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(src + (ft * a.q_stride + fh * D) * C::ELT));
+          ft += step_t;
+          fh += step_h;
+          if (fh >= a.G) {
+            fh -= a.G;
+            ++ft;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) sts16(q_at + box_addr<128>(r0 + i * RPL, ch), v[i]);
         fence_proxy_async_smem();
       }
       if (pair)
@@ -754,7 +768,7 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_tree_wide(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
-  const bool split = a.part_rows <= 128;
+  const bool split = a.max_rows <= 128;
   if (dtype == FP2_BF16 && D == 128) return split ? run<1, 128, true>(a, P, stream) : run<1, 128, false>(a, P, stream);
   if (dtype == FP2_BF16 && D == 64) return split ? run<1, 64, true>(a, P, stream) : run<1, 64, false>(a, P, stream);
   if (dtype == FP2_E4M3 && D == 128) return run<2, 128, false>(a, P, stream);
