@@ -376,6 +376,18 @@ fp2_status fill_evict(const fp2_eviction* p, fp2::EvictArgs& a, int& ranks, size
       !aligned4(p->kv_len_out))
     return invalid("kv_len, mass, mass_out, kept and kv_len_out must be 4-byte aligned");
   if (p->mass_stride < p->max_kv_len) return invalid("mass_stride must be >= max_kv_len");
+  // Other CTAs still read the lengths and weights when the first ones write theirs.
+  const size_t rows = static_cast<size_t>(p->num_seqs) * p->src.num_kv_heads;
+  const auto apart = [](const void* x, size_t xb, const void* y, size_t yb) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return a + xb <= b || b + yb <= a;
+  };
+  const size_t mass_bytes = rows * static_cast<size_t>(p->mass_stride) * 4, out_bytes = rows * p->budget * 4;
+  const size_t len_bytes = static_cast<size_t>(p->num_seqs) * 4;
+  if (!apart(p->kv_len, len_bytes, p->kv_len_out, len_bytes)) return invalid("kv_len_out must not overlap kv_len");
+  if (!apart(p->mass, mass_bytes, p->mass_out, out_bytes) || !apart(p->mass, mass_bytes, p->kept, out_bytes) ||
+      !apart(p->mass_out, out_bytes, p->kept, out_bytes))
+    return invalid("mass, mass_out and kept must not overlap");
   std::memset(&a, 0, sizeof(a));
   a.src = view(p->src);
   a.dst = view(p->dst);
@@ -424,7 +436,7 @@ fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void
   DecodeCtx c;
   FP2_TRY(validate(decode, true, c));
   FP2_TRY(check_scratch(scratch, scratch_bytes, c.bytes));
-  if (out == nullptr || !aligned16(out)) return invalid("out must be a 16-byte aligned pointer");
+  if ((c.T > 0 && out == nullptr) || !aligned16(out)) return invalid("out must be a 16-byte aligned pointer");
   if (!aligned4(lse)) return invalid("lse must be 4-byte aligned");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (c.T == 0) return clear_status(scratch, st);

@@ -324,7 +324,8 @@ FP2_API fp2_status fp2_decode_workspace(const fp2_decode* decode, size_t* scratc
 /* Tree attention (one token per sequence: a plain decode step).
  * out: [T, Hq, d] bf16, 16-byte aligned; lse: [Hq, T] f32 natural-log normaliser, or NULL.  A token
  * that sees no key gets zeros and -infinity.  Keys that a token does not see have no influence on
- * it, whatever their values (NaN included). */
+ * it, whatever their values (NaN included); an infinite or NaN value of a key that it does see makes that
+ * element infinite or NaN. */
 FP2_API fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void* scratch,
                                    size_t scratch_bytes, fp2_stream_t stream);
 
@@ -344,7 +345,8 @@ FP2_API fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, cons
  * lowest index; NaN counts as heaviest).  They are written to rows 0 .. N-1 of dst in ascending order. */
 typedef struct {
   int32_t num_seqs;
-  fp2_cache src, dst;                /* same dtype (any, head_dim 64 or 128), heads and head_dim; no overlap */
+  fp2_cache src, dst;                /* same dtype (any), heads and head_dim.  They may be one pool with other
+                                        pages each; a contiguous one must not overlap the other */
   const int32_t* kv_len;             /* device [num_seqs] */
   int32_t max_kv_len;                /* <= FP2_MAX_CACHE_LEN */
   const float* mass;                 /* device [num_seqs, Hkv, mass_stride] */
@@ -352,7 +354,7 @@ typedef struct {
   int32_t budget, sink, window;      /* budget >= 1, sink + window <= budget */
   float* mass_out;                   /* device [num_seqs, Hkv, budget]: weights of the kept keys, then 0 */
   int32_t* kept;                     /* device [num_seqs, Hkv, budget]: their old indexes, then -1 */
-  int32_t* kv_len_out;               /* device [num_seqs]: N */
+  int32_t* kv_len_out;               /* device [num_seqs]: N; not kv_len itself */
 } fp2_eviction;
 
 FP2_API fp2_status fp2_evict_workspace(const fp2_eviction* eviction, size_t* scratch_bytes);

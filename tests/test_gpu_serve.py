@@ -316,6 +316,66 @@ def test_a_value_that_only_some_tokens_see(qlen):
         assert not fin[qlen] and fin[:qlen].all() and fin[qlen + 1:].all()
 
 
+@pytest.mark.parametrize("qlen", [1, 40])
+def test_a_value_that_is_not_finite_stays_in_its_element(qlen):
+    """NaN in V of a key that every token sees: NaN there, in every token of the group's heads, and nowhere else."""
+    for dtype in ("bf16", "e4m3"):
+        b = Batch(dtype, 128, 8, 2, 64, (300,), (qlen,), None, seed=12)
+        page = int(b.table[0, 1])
+        if dtype == "e4m3":
+            b.v.view(torch.uint8)[page, 7, 1, 37] = 0xFF
+        else:
+            b.v[page, 7, 1, 37] = float("nan")
+        b.attend()
+        torch.cuda.synchronize()
+        bad = torch.isnan(b.out.float()).cpu()
+        want = torch.zeros_like(bad)
+        want[:, 4:, 37] = True
+        assert torch.equal(bad, want) and torch.isfinite(b.lse).all()
+
+
+def test_a_cache_whose_offsets_pass_32_bits():
+    """Pages at the end of caches of 2.3e9 values (K, V and the eviction's)."""
+    from block_sparse_long_pooled_b200 import fp2
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    g = _gen(40)
+    pages, hkv, d = 140000, 2, 128
+    k, v, ko, vo = (torch.empty((pages, 64, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    assert k.numel() > 1 << 31
+    table = torch.arange(pages - 5, pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    n = 300
+    kk, vv = (torch.randn((5 * 64, hkv, d), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+    slots = (pages - 5) * 64 + torch.arange(n, device="cuda")
+    fp2.fp2_rotate(fp2.make_rotate(None, kk[:n], vv[:n], pos, None, None, k, v, slots=slots))
+    q = torch.randn((3, 4, d), generator=g).to(torch.bfloat16).cuda()
+    cache = fp2.make_cache(k, v, table)
+    kv_len = torch.tensor([n], dtype=torch.int32, device="cuda")
+    dec = fp2.make_decode(q, cache, [0, 3], kv_len, n)
+    scratch = fp2.alloc_scratch(fp2.fp2_decode_workspace(dec), "cuda")
+    out, lse = torch.empty_like(q), torch.empty((4, 3), device="cuda")
+    fp2.fp2_tree_attend(dec, out, lse, scratch)
+    vis = R.visible(3, n, None)
+    want, wl, mag, top = R.attend(R.f64(q), R.f64(kk[:n]), R.f64(vv[:n]), d ** -0.5, vis)
+    bo, bl = R.attend_bounds(want, wl, mag, top, d, n, R.HALF["bf16"] ** 2)
+    _within(out, want, bo, "out")
+    mass = torch.zeros((1, hkv, n), device="cuda")
+    fp2.fp2_key_mass(dec, lse, None, mass, scratch)
+    new, bound = R.key_mass(R.f64(q), R.f64(kk[:n]), d ** -0.5, vis, R.f64(lse))
+    _within(mass[0], new, bound + 3 * R.U * new + 1e-37, "mass")
+    mo, kept = torch.empty((1, hkv, 64), device="cuda"), torch.empty((1, hkv, 64), dtype=torch.int32, device="cuda")
+    lo = torch.empty(1, dtype=torch.int32, device="cuda")
+    ev = fp2.make_evict(cache, kv_len, n, mass, 64, 4, 8, fp2.make_cache(ko, vo, table[:, 4:].contiguous()), mo, kept, lo)
+    es = fp2.alloc_scratch(fp2.fp2_evict_workspace(ev), "cuda")
+    fp2.fp2_evict(ev, es)
+    assert _status(es) == (0, 0)
+    for h in range(hkv):
+        idx = R.evict(mass[0, h].cpu().numpy(), n, 64, 4, 8)
+        assert np.array_equal(kept[0, h].cpu().numpy(), idx)
+        assert torch.equal(ko[pages - 1, :, h], kk[idx, h]) and torch.equal(vo[pages - 1, :, h], vv[idx, h])
+
+
 def test_tree_attend_is_repeatable_and_lse_is_optional():
     from block_sparse_long_pooled_b200 import fp2
     b = Batch("bf16", 128, 16, 4, 64, (9000, 100, 4000), (5, 1, 8), "tree", seed=3)
@@ -411,6 +471,19 @@ def test_key_mass(dtype, d, hq, hkv, page, lens, qlens, mask, in_place):
             new, bound = R.key_mass(q, k, b.scale, b.vis[r], lse[:, c])
         # the decayed sum and its sum with the new weight: a rounding each
         _within(got[r, :, :lens[r]], keep + new, bound + 3 * R.U * (np.abs(keep) + new) + 1e-37, f"mass of sequence {r}")
+
+
+def test_key_mass_without_any_token_decays():
+    from block_sparse_long_pooled_b200 import fp2
+    b = Batch("bf16", 128, 8, 2, 16, (200, 0, 33), (0, 0, 0), None, seed=13)
+    mass = torch.rand((3, 2, b.max_len), generator=_gen(1)).cuda()
+    out = torch.full_like(mass, -1.0)
+    fp2.fp2_key_mass(b.handle, b.lse, mass, out, b.scratch, decay=0.5)
+    assert _status(b.scratch) == (0, 0)
+    for r, n in enumerate(b.lens):
+        assert torch.equal(out[r, :, :n], mass[r, :, :n] * 0.5) and (out[r, :, n:] == -1).all()
+    b.attend()     # no rows: nothing to do, and no stale status
+    assert _status(b.scratch) == (0, 0)
 
 
 def test_key_mass_sums_to_the_rows():
@@ -561,6 +634,48 @@ def test_decode_captured_in_a_graph_follows_the_lengths():
         c.check()
 
 
+def test_calls_that_overlap_on_two_streams():
+    """Eager and captured decode, mass and eviction on two streams at once, with scratch of their own."""
+    from block_sparse_long_pooled_b200 import fp2
+    sides = []
+    for i, (dtype, qlens) in enumerate((("bf16", (1, 1, 1)), ("e4m3", (40, 5, 64)))):
+        b = Batch(dtype, 128, 8, 2, 16, (3000, 700, 64), qlens, "tree", seed=50 + i)
+        mass = torch.zeros((3, 2, b.max_len), device="cuda")
+        ko, vo = (torch.zeros((3, 64, 2, 128), dtype=b.k.dtype, device="cuda") for _ in range(2))
+        mo, kept = torch.zeros((3, 2, 64), device="cuda"), torch.zeros((3, 2, 64), dtype=torch.int32, device="cuda")
+        lo = torch.zeros(3, dtype=torch.int32, device="cuda")
+        ev = fp2.make_evict(b.cache, b.kv_len, b.max_len, mass, 64, 2, 8, fp2.make_cache(ko, vo), mo, kept, lo)
+        es = fp2.alloc_scratch(fp2.fp2_evict_workspace(ev), "cuda")
+
+        def step(b=b, mass=mass, ev=ev, es=es):
+            b.attend()
+            fp2.fp2_key_mass(b.handle, b.lse, None, mass, b.scratch)
+            fp2.fp2_evict(ev, es)
+
+        step()
+        torch.cuda.synchronize()
+        b.check()
+        want = [t.clone() for t in (b.out, b.lse, mass, ko.view(torch.uint8), vo.view(torch.uint8), mo, kept, lo)]
+        have = (b.out, b.lse, mass, ko.view(torch.uint8), vo.view(torch.uint8), mo, kept, lo)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        sides.append((step, graph, torch.cuda.Stream(), want, have, b, es))
+    for turn in range(6):
+        for have in (sides[0][4], sides[1][4]):
+            for t in have[:3]:
+                t.zero_()
+        torch.cuda.synchronize()
+        for i, (step, graph, stream, _, _, _, _) in enumerate(sides):
+            with torch.cuda.stream(stream):
+                for _ in range(3):
+                    graph.replay() if (turn + i) % 2 else step()
+        torch.cuda.synchronize()
+        for _, _, _, want, have, b, es in sides:
+            assert all(torch.equal(x, y) for x, y in zip(want, have))    # the same bits every time
+            assert _status(b.scratch) == (0, 0) and _status(es) == (0, 0)
+
+
 def test_serving_loop_from_prompt_to_evicted_cache():
     """Rotate a prompt into a paged cache, prefill it, decode a drafted tree, accumulate the keys' weights, evict,
     and decode on the smaller cache: every step against its 64-bit form on the buffers of the step before."""
@@ -654,3 +769,19 @@ def test_serving_loop_from_prompt_to_evicted_cache():
     bo, bl = R.attend_bounds(want, wl, mag, top, d, budget + 1, R.HALF["bf16"] ** 2)
     _within(o3, want, bo, "decode")
     _within(l3, wl, bl, "decode lse")
+
+
+def test_serving_cases_pass_under_the_checked_build():
+    """The same sources with device-side checks of the rows and positions written: no check may fire."""
+    import os
+    import subprocess
+    import sys
+    from block_sparse_long_pooled_b200 import build, fp2
+    if fp2.fp2_build_flags() == fp2.FP2_BUILD_CHECKED:
+        pytest.skip("this is that run")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider", "-m", "gpu",
+                        "tests/test_gpu_serve.py", "-k", "tree or rotate or mass or evict"], cwd=root,
+                       env=dict(os.environ, FP2_LIBRARY=build.build(checked=True)), capture_output=True, text=True,
+                       timeout=900)
+    assert r.returncode == 0 and " passed" in r.stdout, r.stdout[-4000:] + r.stderr[-2000:]

@@ -226,6 +226,12 @@ def test_evict_refusals(kw, code):
 def test_evict_refuses_overlap_and_small_scratch():
     h = _evict()
     assert fp2.fp2_evict_workspace(h) > 0
+    for out, into in (("kv_len_out", "kv_len"), ("mass_out", "mass"), ("kept", "mass"), ("kept", "mass_out")):
+        bad = _evict()
+        setattr(bad.struct, out, getattr(bad.struct, into))
+        with pytest.raises(fp2.FP2Error) as e:
+            fp2.fp2_evict_workspace(bad)
+        assert e.value.status == INV and "overlap" in str(e.value)
     h.struct.dst.k = h.struct.src.v
     with pytest.raises(fp2.FP2Error) as e:
         fp2.fp2_evict_workspace(h)
