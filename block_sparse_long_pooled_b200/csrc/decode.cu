@@ -1,18 +1,21 @@
-// Attention of drafted tokens over a KV cache (one token: a decode step), and the attention weight
-// that each cached key receives.
+// Attention of drafted tokens over a KV cache (one token: a decode step) with up to 16 query rows per KV
+// head, and the join of what several CTAs have of one sequence.  More rows: tree_wide.cu.
 //
 // Sequence r has kv_len[r] keys, the last q_len of them its drafted tokens; token i sees every key
 // before those and the drafted keys whose bit is set in its mask (no mask: those up to its own).
 //
-// Both kernels read the cache once and little else, so bytes bound them while a KV head has few
-// query rows.  The work is one axis of units (sequence, row tile, key tile), the same for every KV
-// head; kv_len lives on the device, so each CTA scans it and takes an equal share of that axis.  A
-// grid of `groups` x KV heads puts the KV heads of one share side by side in time: their rows are
-// neighbours in DRAM.  An (item = sequence, row tile) that several groups share leaves partial
-// results in scratch, and join_kernel joins them in group order, so results do not depend on
-// timing.  One producer warp brings K/V tiles in by TMA (page by page), consumer warps run
-// mma.sync on them: a tile has 16 to 64 query rows, below the 128 of a tcgen05 tile, and the legacy
-// tensor path keeps pace with HBM up to there.
+// The cache is read once and little else, so bytes bound it.  The work is one axis of units (sequence, row
+// tile, key tile), the same for every KV head; kv_len lives on the device, so each CTA scans it and takes an
+// equal share of that axis.  A grid of `groups` x KV heads puts the KV heads of one share side by side in
+// time: their rows are neighbours in DRAM.  An (item = sequence, row tile) that several groups share leaves
+// partial results in scratch, and join_kernel joins them in group order, so results do not depend on
+// timing.  One producer warp brings K/V tiles in by TMA (page by page), four consumer warps run mma.sync on
+// them: 16 rows are far below the 128 of a tcgen05 tile, and on that path the same calls were slower (three
+// short requests 21 us against 15, a batch of 64 263 us against 247, when that was compared).
+//
+// Measured: 64 requests of 0.5K to 16K bf16 keys, one token each, 241 us, 6.0 TB/s (220 us at the copy's
+// rate); three requests of 190 to 1000 keys 11 us, where the trips to memory one after another count:
+// lengths, tile, statistics of the pieces, their rows.
 #include "decode_device.cuh"
 
 namespace fp2 {
@@ -127,14 +130,14 @@ FP2_DEVICE void stage_q(const DecodeArgs& a, char* q_smem, int t0, int g, int ro
 
 // ------------------------------------------------------------------ tree attention
 
-// Rows of a CTA: WM warps x MT tiles of 16; the 64 keys of a tile go to 4 warps, 16 each.
-template <int DT, int D, int MT, int WM>
+// Up to 16 rows per KV head in one tile; its 64 keys go to 4 warps, 16 each.
+template <int DT, int D>
 struct Tree {
   static constexpr int ELT = DT == 1 ? 2 : 1;
   static constexpr bool F16 = DT == 2;
   static constexpr int WN = 4, TILE = kFewTile;
-  static constexpr int ROWS = 16 * MT * WM;
-  static constexpr int CONSUMERS = 32 * WM * WN;
+  static constexpr int ROWS = kFewRows;
+  static constexpr int CONSUMERS = 32 * WN;
   static constexpr int THREADS = CONSUMERS + 32;
   static constexpr int KV_BYTES = TILE * D * ELT;               // one of K or V
   static constexpr int STAGE_BYTES = 2 * KV_BYTES;
@@ -143,24 +146,23 @@ struct Tree {
   static constexpr int O_BYTES = WN * ROWS * OS * 4;            // of every key warp
   static constexpr int FIXED = 1024 /* alignment */ + Q_BYTES + O_BYTES + WN * ROWS * 8 + (FP2_MAX_SEQS + 1) * 8 +
                                FP2_MAX_SEQS * 4 + 256;
-  static constexpr int CTAS = ROWS <= 32 ? 2 : 1;               // per SM
-  static constexpr int BUDGET = CTAS == 2 ? 113 * 1024 : 226 * 1024;
+  static constexpr int BUDGET = 113 * 1024;                     // two CTAs per SM
   static constexpr int RAW = (BUDGET - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = RAW > 8 ? 8 : RAW;
   static constexpr int SMEM = FIXED + STAGES * STAGE_BYTES;
   // P is held in bf16 against a bf16 V.  Its rounding (2^-9 of each weight) would be as large as the
-  // output's own; where few rows leave the tensor cores idle a second product adds the remainder
-  // P - bf16(P), which costs nothing measurable there.
-  static constexpr bool SPLIT_P = DT == 1 && ROWS <= 32;
+  // output's own; few rows leave the tensor cores idle, so a second product adds the remainder
+  // P - bf16(P), which costs nothing measurable (a batch of 64 requests: 246.7 us with it, 247.7 without).
+  static constexpr bool SPLIT_P = DT == 1;
   // e4m3: P is f16, scaled by 2^8 so that weights down to 2^-22 of the largest keep all 11 bits; the
   // factor leaves with the division by the sum.
   static constexpr float P_BIAS = F16 ? 8.f : 0.f;
 };
 
-template <int DT, int D, int MT, int WM>
-__global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, WM>::CTAS)
+template <int DT, int D>
+__global__ void __launch_bounds__(Tree<DT, D>::THREADS, 2)
     tree_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P) {
-  using C = Tree<DT, D, MT, WM>;
+  using C = Tree<DT, D>;
   extern __shared__ char smem_raw[];
   char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   char* stages = smem;
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
   }
 
   // ---------------- consumers
-  const int wm = warp / C::WN, wn = warp % C::WN;
+  const int wn = warp;  // of the four key warps
   const uint32_t q_base = smem_u32(q_smem);
   int s = 0, it = 0, nth = 0;
   bool alive = true;
@@ -244,21 +246,14 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
     consumer_sync<C::CONSUMERS>();  // the previous piece is written: q_smem, o_smem and ml_smem are free
     stage_q<DT, D, C::CONSUMERS>(a, q_smem, t0, g, row0, C::ROWS, rows, tid);
     consumer_sync<C::CONSUMERS>();
-    // For one row tile of 16 the query fragments stay in registers; two would not fit next to O.
-    uint32_t qf[MT == 1 ? D / 16 : 1][4];
-    if constexpr (MT == 1) {
+    uint32_t qf[D / 16][4];  // the query fragments stay in registers
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        ldsm4(q_addr<DT, D>(q_base, wm * 16 + (lane & 15), 2 * k + (lane >> 4)), qf[k]);
-    }
-    float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
+    for (int k = 0; k < D / 16; ++k) ldsm4(q_addr<DT, D>(q_base, lane & 15, 2 * k + (lane >> 4)), qf[k]);
+    float o[D / 8][4], mx[2], sum[2];
+    mx[0] = mx[1] = neg_inf();
+    sum[0] = sum[1] = 0.f;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      mx[m][0] = mx[m][1] = neg_inf();
-      sum[m][0] = sum[m][1] = 0.f;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
-    }
+    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
     for (int t = p.t0; t < p.t1; ++t) {
       if (alive) alive = mbar_wait(&full[s], (it / C::STAGES) & 1, &abort_flag, &status_word, a.wait_limit_ns);
@@ -275,96 +270,74 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
       const bool plain = here == 0xFFFFu && j0 + 16 <= base;
 
       // S = Q K^T, 16 rows x 16 keys per row tile
-      float sc[MT][2][4];
+      float sc[2][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) sc[m][n][0] = sc[m][n][1] = sc[m][n][2] = sc[m][n][3] = 0.f;
+      for (int n = 0; n < 2; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        uint32_t b[4];
         if constexpr (!C::F16) {
+          uint32_t b[4];
           ldsm4(tile_addr<C::TILE>(k_at, wn * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b);
-        } else {
-          if ((k & 1) == 0) continue;  // two groups of 16 values at a time, below
-        }
-        if constexpr (!C::F16) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            uint32_t q4[4];
-            const uint32_t(&qa)[4] = MT == 1 ? qf[k * (MT == 1)] : q4;
-            if constexpr (MT != 1)
-              ldsm4(q_addr<DT, D>(q_base, (wm * MT + m) * 16 + (lane & 15), 2 * k + (lane >> 4)), q4);
-            mma<false>(sc[m][0], qa, b[0], b[1]);
-            mma<false>(sc[m][1], qa, b[2], b[3]);
-          }
-        } else {
-          // matrices: keys 0-7 and 8-15 of chunk k - 1, then of chunk k
-          ldsm4(tile_addr<C::TILE>(k_at, wn * 16 + (lane & 15), k - 1 + (lane >> 4)), b);
+          mma<false>(sc[0], qf[k], b[0], b[1]);
+          mma<false>(sc[1], qf[k], b[2], b[3]);
+        } else if ((k & 1) == 0) {
+          // matrices: keys 0-7 and 8-15 of chunk k, then of chunk k + 1
+          uint32_t b[4];
+          ldsm4(tile_addr<C::TILE>(k_at, wn * 16 + (lane & 15), k + (lane >> 4)), b);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t b00, b01, b10, b11;
             widen_k(b[2 * c], b00, b01);
             widen_k(b[2 * c + 1], b10, b11);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              uint32_t q4[4];
-              const uint32_t(&qa)[4] = MT == 1 ? qf[(k - 1 + c) * (MT == 1)] : q4;
-              if constexpr (MT != 1)
-                ldsm4(q_addr<DT, D>(q_base, (wm * MT + m) * 16 + (lane & 15), 2 * (k - 1 + c) + (lane >> 4)), q4);
-              mma<true>(sc[m][0], qa, b00, b01);
-              mma<true>(sc[m][1], qa, b10, b11);
-            }
+            mma<true>(sc[0], qf[k + c], b00, b01);
+            mma<true>(sc[1], qf[k + c], b10, b11);
           }
         }
       }
 
       // Masks, the running maximum and the weights
-      uint32_t pf[MT][4], pl[MT][4];
-      uint32_t vis[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        vis[m][0] = vis[m][1] = here;
-        if (!plain) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = row0 + (wm * MT + m) * 16 + (lane >> 2) + 8 * i;
-            vis[m][i] = row < rows && keys > 0 ? here & seen16(token_mask(a, t0, row / a.G), j0, base) : 0u;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (!((vis[m][i] >> (8 * n + 2 * (lane & 3) + e)) & 1u)) sc[m][n][2 * i + e] = neg_inf();
-          }
-        }
+      uint32_t pf[4], pl[4];
+      uint32_t vis[2];
+      vis[0] = vis[1] = here;
+      if (!plain) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float v = fmaxf(fmaxf(sc[m][0][2 * i], sc[m][0][2 * i + 1]), fmaxf(sc[m][1][2 * i], sc[m][1][2 * i + 1]));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-          const float now = fmaxf(mx[m][i], v);
-          if (__any_sync(0xFFFFFFFFu, now > mx[m][i])) {
-            // exp2(-inf) = 0 clears a row that had seen nothing; a row that still has keeps its zeros.
-            const float f = now == neg_inf() ? 1.f : fast_exp2((mx[m][i] - now) * a.scale_log2);
-            sum[m][i] *= f;
+          const int row = row0 + (lane >> 2) + 8 * i;
+          vis[i] = row < rows && keys > 0 ? here & seen16(token_mask(a, t0, row / a.G), j0, base) : 0u;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              o[m][n][2 * i] *= f;
-              o[m][n][2 * i + 1] *= f;
-            }
-            mx[m][i] = now;
-          }
-          const float off = now == neg_inf() ? 0.f : C::P_BIAS - now * a.scale_log2;
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float e0 = fast_exp2(fmaf(sc[m][n][2 * i], a.scale_log2, off));
-            const float e1 = fast_exp2(fmaf(sc[m][n][2 * i + 1], a.scale_log2, off));
-            sum[m][i] += e0 + e1;
-            const uint32_t w = C::F16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
-            pf[m][2 * n + i] = w;
-            if constexpr (C::SPLIT_P)
-              pl[m][2 * n + i] = pack_bf16x2(e0 - __uint_as_float(w << 16), e1 - __uint_as_float(w & 0xFFFF0000u));
+            for (int e = 0; e < 2; ++e)
+              if (!((vis[i] >> (8 * n + 2 * (lane & 3) + e)) & 1u)) sc[n][2 * i + e] = neg_inf();
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
+        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+        const float now = fmaxf(mx[i], v);
+        if (__any_sync(0xFFFFFFFFu, now > mx[i])) {
+          // exp2(-inf) = 0 clears a row that had seen nothing; a row that still has keeps its zeros.
+          const float f = now == neg_inf() ? 1.f : fast_exp2((mx[i] - now) * a.scale_log2);
+          sum[i] *= f;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[n][2 * i] *= f;
+            o[n][2 * i + 1] *= f;
           }
+          mx[i] = now;
+        }
+        const float off = now == neg_inf() ? 0.f : C::P_BIAS - now * a.scale_log2;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float e0 = fast_exp2(fmaf(sc[n][2 * i], a.scale_log2, off));
+          const float e1 = fast_exp2(fmaf(sc[n][2 * i + 1], a.scale_log2, off));
+          sum[i] += e0 + e1;
+          const uint32_t w = C::F16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+          pf[2 * n + i] = w;
+          if constexpr (C::SPLIT_P)
+            pl[2 * n + i] = pack_bf16x2(e0 - __uint_as_float(w << 16), e1 - __uint_as_float(w & 0xFFFF0000u));
         }
       }
 
@@ -407,29 +380,23 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
               for (int e = 0; e < 4; ++e)
                 f[e] = (kind == 0 ? bad[e] == EXP : kind == 1 ? bad[e] == (EXP | 0x8000u) : (bad[e] & 0x7FFFu) > EXP)
                            ? ONE : 0u;
+              uint32_t va[4];
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                uint32_t va[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t two = vis[m][e & 1] >> (2 * (lane & 3) + 8 * (e >> 1));
-                  va[e] = ((two & 1u) ? ONE : 0u) | ((two & 2u) ? ONE << 16 : 0u);
-                }
-                float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-                mma<C::F16>(cnt, va, f[0] | (f[1] << 16), f[2] | (f[3] << 16));
-                const float add = kind == 0 ? pos_inf() : kind == 1 ? neg_inf() : __uint_as_float(0x7FFFFFFFu);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (cnt[e] > 0.f) o[m][n][e] += add;
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t two = vis[e & 1] >> (2 * (lane & 3) + 8 * (e >> 1));
+                va[e] = ((two & 1u) ? ONE : 0u) | ((two & 2u) ? ONE << 16 : 0u);
               }
+              float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+              mma<C::F16>(cnt, va, f[0] | (f[1] << 16), f[2] | (f[3] << 16));
+              const float add = kind == 0 ? pos_inf() : kind == 1 ? neg_inf() : __uint_as_float(0x7FFFFFFFu);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (cnt[e] > 0.f) o[n][e] += add;
             }
           }
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma<C::F16>(o[m][n], pf[m], b0, b1);
-          if constexpr (C::SPLIT_P) mma<C::F16>(o[m][n], pl[m], b0, b1);
-        }
+        mma<C::F16>(o[n], pf, b0, b1);
+        if constexpr (C::SPLIT_P) mma<C::F16>(o[n], pl, b0, b1);
       };
       if constexpr (!C::F16) {
 #pragma unroll
@@ -462,28 +429,26 @@ __global__ void __launch_bounds__(Tree<DT, D, MT, WM>::THREADS, Tree<DT, D, MT, 
     // The four key warps lay down what they have of each row; whoever writes the row adds it up.  (Adding
     // it up in shared memory warp by warp cost four barriers more, 0.6 us of a decode step's 6.)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < 2; ++i) {
+      float x = sum[i];
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+      const int row = (lane >> 2) + 8 * i;
+      if ((lane & 3) == 0) ml_smem[wn * C::ROWS + row] = make_float2(mx[i], x);
+      if (row0 + row >= rows) continue;
+      float* dst = o_smem + (wn * C::ROWS + row) * C::OS;
+      if constexpr (!C::F16) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = sum[m][i];
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-        const int row = (wm * MT + m) * 16 + (lane >> 2) + 8 * i;
-        if ((lane & 3) == 0) ml_smem[wn * C::ROWS + row] = make_float2(mx[m][i], x);
-        if (row0 + row >= rows) continue;
-        float* dst = o_smem + (wn * C::ROWS + row) * C::OS;
-        if constexpr (!C::F16) {
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(dst + 8 * n + 2 * (lane & 3)) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+      } else {
+        // columns 2q, 2q+1 of the even and odd accumulators are d = 4q, 4q+2 and 4q+1, 4q+3
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2*>(dst + 8 * n + 2 * (lane & 3)) = make_float2(o[m][n][2 * i], o[m][n][2 * i + 1]);
-        } else {
-          // columns 2q, 2q+1 of the even and odd accumulators are d = 4q, 4q+2 and 4q+1, 4q+3
-#pragma unroll
-          for (int n = 0; n < D / 16; ++n)
-            *reinterpret_cast<float4*>(dst + 16 * n + 4 * (lane & 3)) =
-                make_float4(o[m][2 * n][2 * i], o[m][2 * n + 1][2 * i], o[m][2 * n][2 * i + 1], o[m][2 * n + 1][2 * i + 1]);
-        }
+        for (int n = 0; n < D / 16; ++n)
+          *reinterpret_cast<float4*>(dst + 16 * n + 4 * (lane & 3)) =
+              make_float4(o[2 * n][2 * i], o[2 * n + 1][2 * i], o[2 * n][2 * i + 1], o[2 * n + 1][2 * i + 1]);
       }
+    }
     consumer_sync<C::CONSUMERS>();
 
     // Out: the whole item, or this group's part of it.
@@ -627,9 +592,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
 
 template <int DT, int D>
 cudaError_t run_tree(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
-  using C = Tree<DT, D, 1, 1>;
+  using C = Tree<DT, D>;
   static_assert(C::STAGES >= 2, "tiles must fit twice");
-  const auto kernel = tree_kernel<DT, D, 1, 1>;
+  const auto kernel = tree_kernel<DT, D>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_chained(kernel, dim3(a.groups * a.Hkv), C::THREADS, C::SMEM, stream, 1, a, P);

@@ -16,8 +16,13 @@
 // warp walks the heads of one token, first Q's, then K's, then V's.  Bytes should bound it, but at 335
 // million values the instructions count as much: norm weight, cosine and sine are multiplied once per
 // token into four factors a pair, so that a head costs a thread two products, two fused ones and the
-// norm's factor for each pair, in packed fp32 pairs.  With few tokens the heads are spread over more
-// warps instead (run_rotate).
+// norm's factor for each pair, in packed fp32 pairs; and the values come four steps ahead through shared
+// memory, as loads into registers left the SM waiting (250 and 220 us).  With few tokens the heads are
+// spread over more warps instead (run_rotate).
+//
+// Measured: 64K tokens of 32 + 4 + 4 heads, norms, bf16 to e4m3 pages: 196 us, 5.1 TB/s (154 us at the
+// copy's rate); some 2,500 warp instructions a token issue in three quarters of the cycles.  Eight tokens:
+// 2.9 us in a graph, 4 to 5 us by call, which is the host's time.
 #include "fp2_device.cuh"
 #include "serve_kernels.h"
 
@@ -26,9 +31,9 @@ namespace fp2 {
 namespace {
 
 constexpr int kRotThreads = 128;
-#ifndef MINB
-#define MINB 7
-#endif
+// Blocks per SM that the registers are cut for: 7 of bf16 (72 registers; 6 or 8 were 1 and 4 % slower on the
+// prompt below), 4 of f32 (with 5 an odd chunk of 1537 tokens took 7.2 us instead of 6.2).
+constexpr int blocks_per_sm(int din) { return din == 0 ? 4 : 7; }
 
 // Eight values from four words of two bf16, or eight floats.
 template <int DIN>
@@ -91,7 +96,7 @@ FP2_DEVICE float4 lds_f4(uint32_t addr) {
 
 // DIN / DOUT: 0 f32, 1 bf16, 2 e4m3.
 template <int DIN, int DOUT, int D, bool INTER>
-__global__ void __launch_bounds__(kRotThreads, DIN == 0 ? 4 : MINB) rotate_kernel(const __grid_constant__ RotateArgs a) {
+__global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel(const __grid_constant__ RotateArgs a) {
   grid_launch_next();
   grid_wait();
   constexpr int TPH = D / 16;                          // threads per head

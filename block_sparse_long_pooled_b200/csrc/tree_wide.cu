@@ -11,10 +11,14 @@
 // Per key tile and stream: S = Q K^T into TMEM; one thread per row takes the row's 64 scores into
 // registers, masks them, raises the running maximum only when it grew by more than 2^8 (then O is
 // rescaled in TMEM), and writes P over S in TMEM; O += P V.  A stream has two buffers of 64 columns:
-// S(j + 1) is computed while the softmax works on S(j), so that the exponentials, which bound the
-// wide calls (16 a cycle and SM: 512 cycles for 128 x 64, the products take 448), never wait.  With
-// one buffer of 128 keys they stood still for the products of every tile: 299 us against MEASURED us
-// for eight trees of 33 to 64 tokens on an e4m3 cache.
+// S(j + 1) is computed while the softmax works on S(j).  With one buffer of 128 keys the exponentials stood
+// still for the products of every tile: 299 us for eight trees of 33 to 64 tokens by 8 heads on an e4m3
+// cache of 9K to 33K keys, now 148 (658 TFLOP/s).  There a pair's tile takes about 2,300 cycles.  The
+// exponentials (16 a cycle and SM) would need 1,024 of them and the products 900; taking either away saves
+// little, and half of them on the FMA pipe cost 10 us.  What bounds it is the chain: some 1,600 cycles in
+// which a stream's issuing warp waits, issues and commits S and O, and the softmax's loads, votes and
+// barriers around its arithmetic.  With few rows the cache's bytes bound the call: 7 tokens by 4 heads at
+// 128K bf16 keys 98 us, 82 of them in the tiles, at 6.5 TB/s.
 //
 // P in bf16 would be off by up to 2^-9 of each weight, as much as the output's own rounding; with at
 // most 128 rows the cache's bytes bound the call, so there a second product adds P - bf16(P), for
@@ -44,6 +48,10 @@ struct Wide {
   static constexpr int V16_BYTES = E4 ? TILE * D * 2 : 0;
   static constexpr int STAGES = E4 || D == 64 ? 6 : 4;
   static constexpr int COPIES = 4;                // of V in f16
+  // Even, both: in parity a stream then meets every second stage only, and each of its phases.  With an odd
+  // ring a stage would belong to the streams in turn, and a stream that waits for its next phase there would
+  // take its own last one, of the same parity, for it.
+  static_assert(STAGES % 2 == 0 && COPIES % 2 == 0, "rings of two streams");
   static constexpr int KIND_QK = E4 ? 2 : 1, UK = 32 / ELT;
   static constexpr uint32_t FMT_QK = E4 ? 0u : 1u, FMT_PV = E4 ? 0u : 1u;  // e4m3 / bf16; f16 / bf16
   static constexpr uint32_t IDESC_S = make_idesc(FMT_QK, FMT_QK, 0, 0, 128, TILE);

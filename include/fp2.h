@@ -396,6 +396,8 @@ FP2_API fp2_status fp2_discover_static(const fp2_problem* problem, const fp2_spa
  *                              hand-off counters, so the consumer's check of that load fails and
  *                              the status word gets FP2_DEV_CHECK.  The data path is unchanged;
  *                              the normal build ignores it.
+ * The first two also hold for fp2_tree_attend and fp2_key_mass on BF16 and E4M3 caches: the limit of
+ * their waits, and every producer skips the K load of its local key tile `value`.
  * Returns FP2_ERR_INVALID_ARG for an unknown key or a value out of range. */
 #define FP2_DEBUG_WAIT_LIMIT_NS 1
 #define FP2_DEBUG_WITHHOLD_K_TILE 2

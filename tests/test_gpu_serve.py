@@ -237,11 +237,11 @@ class Batch:
         fp2.fp2_tree_attend(self.handle, self.out, self.lse, self.scratch, stream=stream)
 
     def p_half(self):
-        # e4m3: weights are f16.  bf16: two bf16 halves up to 32 rows per KV head, one above.
+        # e4m3: weights are f16.  bf16: two bf16 halves when no sequence has over 128 rows per KV head, else one.
         if self.dtype == "e4m3":
             return R.HALF["f16"]
         rows = max(self.qlens) * self.hq // self.hkv
-        return R.HALF["bf16"] ** 2 if rows <= 32 else R.HALF["bf16"]
+        return R.HALF["bf16"] ** 2 if rows <= 128 else R.HALF["bf16"]
 
     def check(self):
         assert _status(self.scratch) == (0, 0)
