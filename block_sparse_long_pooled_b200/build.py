@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp2.so")
 CHECKED_LIB = os.path.join(HERE, "libfp2_checked.so")
 SOURCES = ["fp2_api.cu", "pool.cu", "discover.cu", "attention.cu", "fp2_noalloc.cu", "fp2_serve.cu", "rotate.cu",
-           "decode.cu", "tree_wide.cu", "key_mass.cu", "evict.cu"]
+           "decode.cu", "tree_wide.cu", "key_mass.cu", "decode_f32.cu", "evict.cu"]
 HEADERS = ["fp2_device.cuh", "fp2_kernels.h", "fp2_plan.h", "serve_kernels.h", "decode_device.cuh",
            os.path.join("..", "..", "include", "fp2.h")]
 

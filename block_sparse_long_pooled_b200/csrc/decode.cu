@@ -50,29 +50,6 @@ template <int N>
 FP2_DEVICE void consumer_sync() {  // the N consumer threads only (barrier 1)
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
-struct Piece {  // key tiles [t0, t1) of one item
-  int r, rt, t0, t1, tiles;
-};
-
-// The piece that starts at unit u (u < u1 <= pre[num_seqs]).
-template <int TILE>
-FP2_DEVICE Piece piece_at(const long long* pre, const int* len, int num_seqs, long long u, long long u1) {
-  int lo = 0, hi = num_seqs - 1;  // the last r with pre[r] <= u: sequences without rows have no units
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= u) lo = mid; else hi = mid - 1;
-  }
-  Piece p;
-  p.r = lo;
-  p.tiles = len[lo] <= 0 ? 1 : (len[lo] + TILE - 1) / TILE;
-  const int rem = static_cast<int>(u - pre[lo]);
-  p.rt = rem / p.tiles;
-  p.t0 = rem - p.rt * p.tiles;
-  const long long left = u1 - u;
-  p.t1 = p.tiles - p.t0 <= left ? p.tiles : p.t0 + static_cast<int>(left);
-  return p;
-}
-
 // ------------------------------------------------------------------ operand fragments
 
 // Address of 16-byte chunk c (of the D * ELT / 16 of a row) of row k in a K/V tile: boxes of 128
@@ -583,9 +560,15 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
   const float f = total == 0.f ? 0.f : a.v_descale / total;
   // the word of the attention CTA with this index, written before this kernel went on
   if (!fp2_check(row < a.T && h < a.Hq, a.scratch + kStatusFirst + blockIdx.x)) return;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (row * a.Hq + h) * D + lane * V);
+  const int64_t to = (row * a.Hq + h) * D + lane * V;
+  if (a.out_f32) {
 #pragma unroll
-  for (int e = 0; e < V / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * f, acc[2 * e + 1] * f);
+    for (int e = 0; e < V; ++e) static_cast<float*>(a.out)[to + e] = acc[e] * f;
+  } else {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * f, acc[2 * e + 1] * f);
+  }
   if (lane == 0 && a.lse != nullptr)
     a.lse[static_cast<int64_t>(h) * a.T + row] = total == 0.f ? neg_inf() : (top + log2f(total)) * kLn2;
 }

@@ -79,6 +79,29 @@ FP2_DEVICE int group_of(long long units, int groups, long long u) {
   return static_cast<int>(((u + 1) * groups - 1) / units);
 }
 
+struct Piece {  // key tiles [t0, t1) of one item
+  int r, rt, t0, t1, tiles;
+};
+
+// The piece that starts at unit u (u < u1 <= pre[num_seqs]).
+template <int TILE>
+FP2_DEVICE Piece piece_at(const long long* pre, const int* len, int num_seqs, long long u, long long u1) {
+  int lo = 0, hi = num_seqs - 1;  // the last r with pre[r] <= u: sequences without rows have no units
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  Piece p;
+  p.r = lo;
+  p.tiles = len[lo] <= 0 ? 1 : (len[lo] + TILE - 1) / TILE;
+  const int rem = static_cast<int>(u - pre[lo]);
+  p.rt = rem / p.tiles;
+  p.t0 = rem - p.rt * p.tiles;
+  const long long left = u1 - u;
+  p.t1 = p.tiles - p.t0 <= left ? p.tiles : p.t0 + static_cast<int>(left);
+  return p;
+}
+
 // The CTA's status bits go to a word of its own in scratch (see serve_kernels.h); every thread
 // calls it, with nothing of the CTA's left to do.
 FP2_DEVICE void store_status(const DecodeArgs& a, const uint32_t* status) {

@@ -185,7 +185,7 @@ fp2_status run_rotate(const fp2_rotation* p, uint32_t* status_dev, cudaStream_t 
 
 struct DecodeCtx {
   int G = 0, T = 0, max_rows = 0;
-  bool few = true;                      // which tree attention kernel
+  bool f32 = false, few = true;         // which tree attention kernel
   int part_rows = 16, groups_tree = 1, groups_mass = 1;
   size_t off_desc = 0, off_ml = 0, off_o = 0, bytes = 0;
   float scale = 0.f;
@@ -210,7 +210,6 @@ fp2_status validate(const fp2_decode* p, bool need_v, DecodeCtx& c) {
   if (p->max_kv_len < 0) return invalid("max_kv_len must be >= 0");
   if (p->max_kv_len > FP2_MAX_CACHE_LEN) return unsupported("max_kv_len above FP2_MAX_CACHE_LEN");
   FP2_TRY(check_cache(p->cache, p->num_seqs, p->max_kv_len, need_v));
-  if (p->cache.dtype == FP2_F32) return unsupported("decode needs a BF16 or E4M3 cache");
   if (p->num_q_heads <= 0 || p->num_q_heads % p->cache.num_kv_heads != 0)
     return invalid("num_q_heads must be a positive multiple of num_kv_heads");
   c.G = p->num_q_heads / p->cache.num_kv_heads;
@@ -240,13 +239,16 @@ fp2_status validate(const fp2_decode* p, bool need_v, DecodeCtx& c) {
       return invalid("q_stride_tok must be >= heads * head_dim and a multiple of 16 bytes");
     if (!aligned8(p->tree_mask)) return invalid("tree_mask must be 8-byte aligned");
   }
-  // Two CTAs of the few-rows kernel share an SM, one of the wide kernel fills it.
+  // Two CTAs of the few-rows kernel share an SM, three of the F32 kernel while rows leave them room, one of the wide
+  // kernel fills it.
   const int sms = num_sms();
-  c.few = c.max_rows <= fp2::kFewRows;
+  c.f32 = p->cache.dtype == FP2_F32;
+  c.few = c.f32 || c.max_rows <= fp2::kFewRows;
   c.part_rows = c.few ? fp2::kFewRows : (c.max_rows <= 128 ? 128 : 256);
-  c.groups_tree = c.few ? groups_for(p, c.G, fp2::kFewTile, fp2::kFewRows, 0, sms * 2)
+  c.groups_tree = c.few ? groups_for(p, c.G, fp2::kFewTile, fp2::kFewRows, 0, sms * (c.f32 && c.max_rows <= 4 ? 3 : 2))
                         : groups_for(p, c.G, fp2::kWideTile, 128, 0, sms);
-  c.groups_mass = groups_for(p, c.G, fp2::kMassTile, fp2::kMassRows / c.G * c.G, 1, sms);
+  c.groups_mass = c.f32 ? groups_for(p, c.G, fp2::kMassTile, FP2_MAX_DRAFT * c.G, 1, sms * 4)
+                        : groups_for(p, c.G, fp2::kMassTile, fp2::kMassRows / c.G * c.G, 1, sms);
   const size_t ctas = static_cast<size_t>(c.groups_tree) * p->cache.num_kv_heads;
   const size_t words = std::max(ctas, static_cast<size_t>(c.groups_mass) * p->cache.num_kv_heads);
   c.off_desc = FP2_SCRATCH_STATUS_BYTES + align_up(words * 4);
@@ -301,7 +303,7 @@ fp2_status encode_q(CUtensorMap* m, const fp2_decode* p, int T, int G, int token
 fp2_status fill_decode(const fp2_decode* p, const DecodeCtx& c, void* scratch, fp2::DecodeArgs& a,
                        fp2::DecodePlan& P) {
   std::memset(&a, 0, sizeof(a));
-  FP2_TRY(encode_cache(&a.tm_k, p->cache, p->cache.k));
+  if (!c.f32) FP2_TRY(encode_cache(&a.tm_k, p->cache, p->cache.k));
   P.num_seqs = p->num_seqs;
   std::memcpy(P.q_off, p->cu_seqlens_q_host, sizeof(int32_t) * (p->num_seqs + 1));
   a.q = p->q;
@@ -309,6 +311,11 @@ fp2_status fill_decode(const fp2_decode* p, const DecodeCtx& c, void* scratch, f
   a.kv_len = p->kv_len;
   a.max_kv_len = p->max_kv_len;
   a.page_table = p->cache.page_table;
+  a.max_rows = c.max_rows;
+  a.k_ptr = p->cache.k;
+  a.v_ptr = p->cache.v;
+  a.kv_stride = p->cache.stride_tok;
+  a.kv_stride_outer = p->cache.stride_outer;
   a.page_size = p->cache.rows;
   while (a.page_table != nullptr && (2 << a.page_shift) <= a.page_size) ++a.page_shift;
   a.box_rows = box_rows(p->cache);
@@ -443,7 +450,7 @@ fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void
   fp2::DecodeArgs a;
   fp2::DecodePlan P;
   FP2_TRY(fill_decode(decode, c, scratch, a, P));
-  FP2_TRY(encode_cache(&a.tm_v, decode->cache, decode->cache.v));
+  if (!c.f32) FP2_TRY(encode_cache(&a.tm_v, decode->cache, decode->cache.v));
   char* base = static_cast<char*>(scratch);
   a.groups = c.groups_tree;
   a.out = out;
@@ -452,14 +459,12 @@ fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void
   a.part_ml = reinterpret_cast<float2*>(base + c.off_ml);
   a.part_o = reinterpret_cast<float*>(base + c.off_o);
   a.part_rows = c.part_rows;
-  a.max_rows = c.max_rows;
-  a.v_ptr = decode->cache.v;
-  a.kv_stride = decode->cache.stride_tok;
-  a.kv_stride_outer = decode->cache.stride_outer;
+  a.out_f32 = c.f32 ? 1 : 0;
   if (!c.few && decode->cache.dtype == FP2_E4M3) a.v_descale *= 256.f;  // tree_wide.cu works on V * 2^-8
   const int D = decode->cache.head_dim;
-  FP2_TRY(launched(c.few ? fp2::launch_tree_few(decode->cache.dtype, D, a, P, st)
-                         : fp2::launch_tree_wide(decode->cache.dtype, D, a, P, st)));
+  FP2_TRY(launched(c.f32   ? fp2::launch_tree_f32(a, P, st)
+                   : c.few ? fp2::launch_tree_few(decode->cache.dtype, D, a, P, st)
+                           : fp2::launch_tree_wide(decode->cache.dtype, D, a, P, st)));
   if (a.groups == 1) return FP2_OK;  // no item is split
   return launched(fp2::launch_tree_join(D, c.max_rows, a, P, st));
 }
@@ -481,7 +486,7 @@ fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, const float*
   FP2_TRY(fill_decode(decode, c, scratch, a, P));
   a.groups = c.groups_mass;
   a.pass_tokens = fp2::kMassRows / c.G;
-  if (c.T > 0)
+  if (!c.f32 && c.T > 0)
     FP2_TRY(encode_q(&a.tm_q, decode, c.T, c.G, a.pass_tokens));
   else
     a.tm_q = a.tm_k;  // there are no rows to load: see key_mass.cu
@@ -491,6 +496,7 @@ fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, const float*
   a.mass_stride = mass_stride;
   a.mass_len = mass_len;
   a.decay = decay;
+  if (c.f32) return launched(fp2::launch_mass_f32(a, P, st));
   return launched(fp2::launch_key_mass(decode->cache.dtype, decode->cache.head_dim, a, P, st));
 }
 

@@ -98,14 +98,16 @@ struct DecodeArgs {
   float v_descale;
   int groups;                 // CTAs per KV head
   // tree attention
-  void* out;                  // [T, Hq, d] bf16
+  void* out;                  // [T, Hq, d] bf16, or f32
+  int out_f32;
   float* lse;                 // [Hq, T] or NULL
   int4* desc;                 // [groups] {slot of the first piece of a split item or -1, sequence, row tile, pieces}
   float2* part_ml;            // [groups * Hkv * 2][rows] running maximum (log2 units) and sum
   float* part_o;              // [groups * Hkv * 2][part_rows][d]
   int part_rows;              // rows of a partial result
   int max_rows;               // most query rows per (sequence, KV head)
-  const void* v_ptr;          // V once more, in elements, for values that the products leave out
+  const void* k_ptr;          // the cache without its maps: decode_f32.cu, and (V) values that the wide kernel's
+  const void* v_ptr;          // products leave out
   int64_t kv_stride, kv_stride_outer;
   // key mass
   const float* lse_in;
@@ -124,6 +126,8 @@ struct DecodeArgs {
 constexpr int kFewRows = 16;
 cudaError_t launch_tree_few(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
 cudaError_t launch_tree_wide(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
+cudaError_t launch_tree_f32(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
+cudaError_t launch_mass_f32(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
 cudaError_t launch_tree_join(int D, int max_rows, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
 cudaError_t launch_key_mass(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream);
 constexpr int kFewTile = 64;     // keys of a tile: decode.cu

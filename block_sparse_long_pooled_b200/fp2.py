@@ -498,7 +498,7 @@ class Decode(_Handle):
         tokens, heads, dim = tensors[0].shape
         self.out_shape, self.lse_shape = (tokens, heads, dim), (heads, tokens)
         self.seqs, self.kv_heads, self.has_v = struct.num_seqs, struct.cache.num_kv_heads, bool(struct.cache.v)
-        self.types = torch.bfloat16, torch.float32, torch.int32
+        self.types = torch.float32 if struct.cache.dtype == FP2_F32 else torch.bfloat16, torch.float32, torch.int32
 
 
 class Eviction(_Handle):
@@ -679,11 +679,12 @@ def fp2_decode_workspace(decode: Decode) -> int:
 
 
 def fp2_tree_attend(decode: Decode, out, lse, scratch, stream=None):
-    """Attention of the new tokens over their caches.  out [T, Hq, d] bf16; lse [Hq, T] f32 or None."""
+    """Attention of the new tokens over their caches.  out [T, Hq, d] bf16 (f32 over an F32 cache); lse
+    [Hq, T] f32 or None."""
     if not decode.has_v:
         raise ValueError("the cache has no v")
-    bf16, f32, _ = decode.types
-    decode.call(decode.lib.fp2_tree_attend, (decode.pointer(out, bf16, decode.out_shape, "out"),
+    wide, f32, _ = decode.types
+    decode.call(decode.lib.fp2_tree_attend, (decode.pointer(out, wide, decode.out_shape, "out"),
                                              decode.pointer(lse, f32, decode.lse_shape, "lse"),
                                              *decode.space(scratch)), stream)
 

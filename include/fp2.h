@@ -310,7 +310,7 @@ typedef struct {
   int64_t q_stride_tok;
   float q_descale, k_descale, v_descale;  /* value = stored * descale; 1.0 unless E4M3 */
   float softmax_scale;               /* 0 -> 1/sqrt(head_dim) */
-  fp2_cache cache;                   /* FP2_BF16, or FP2_E4M3 with head_dim 128 */
+  fp2_cache cache;
   const int32_t* kv_len;             /* device [num_seqs]: keys per sequence, drafted ones included */
   int32_t max_kv_len;                /* no kv_len is above it; <= FP2_MAX_CACHE_LEN */
   const uint64_t* tree_mask;         /* device [T] or NULL.  Bit b of a token's word: it sees drafted key b
@@ -322,7 +322,7 @@ typedef struct {
 FP2_API fp2_status fp2_decode_workspace(const fp2_decode* decode, size_t* scratch_bytes);
 
 /* Tree attention (one token per sequence: a plain decode step).
- * out: [T, Hq, d] bf16, 16-byte aligned; lse: [Hq, T] f32 natural-log normaliser, or NULL.  A token
+ * out: [T, Hq, d] bf16 (f32 over an F32 cache), 16-byte aligned; lse: [Hq, T] f32 natural-log normaliser, or NULL.  A token
  * that sees no key gets zeros and -infinity.  Keys that a token does not see have no influence on
  * it, whatever their values (NaN included); an infinite or NaN value of a key that it does see makes that
  * element infinite or NaN. */
@@ -396,8 +396,8 @@ FP2_API fp2_status fp2_discover_static(const fp2_problem* problem, const fp2_spa
  *                              hand-off counters, so the consumer's check of that load fails and
  *                              the status word gets FP2_DEV_CHECK.  The data path is unchanged;
  *                              the normal build ignores it.
- * The first two also hold for fp2_tree_attend and fp2_key_mass on BF16 and E4M3 caches: the limit of
- * their waits, and every producer skips the K load of its local key tile `value`.
+ * The first two also hold for fp2_tree_attend and fp2_key_mass (F32 caches apart, whose kernels wait for
+ * no barrier): the limit of their waits, and every producer skips the K load of its local key tile `value`.
  * Returns FP2_ERR_INVALID_ARG for an unknown key or a value out of range. */
 #define FP2_DEBUG_WAIT_LIMIT_NS 1
 #define FP2_DEBUG_WITHHOLD_K_TILE 2

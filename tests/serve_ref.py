@@ -109,10 +109,10 @@ def score_error(top, d):
     return (d + 2) * 2 * U * top
 
 
-def attend_bounds(out, lse, mag, top, d, n, p_half):
-    """p_half: half a step of the type that the weights are rounded to."""
+def attend_bounds(out, lse, mag, top, d, n, p_half, dtype="bf16"):
+    """p_half: half a step of the type that the weights are rounded to; dtype: of the output."""
     e = 2 * score_error(top, d) + 2 * (2 * top + 4) * 2 * U + (n + 16) * 2 * U + p_half    # [Hq, Q]
-    b_out = HALF["bf16"] * np.abs(out) * (1 + 2.0 ** -7) + e.T[..., None] * mag * (1 + 2.0 ** -7) + n * 2.0 ** -33 * mag
+    b_out = HALF[dtype] * np.abs(out) * (1 + 2.0 ** -7) + e.T[..., None] * mag * (1 + 2.0 ** -7) + n * 2.0 ** -33 * mag
     b_lse = score_error(top, d) + (2 * top + 4 + n + 16) * 2 * U + np.abs(np.where(np.isfinite(lse), lse, 0)) * 4 * U
     return b_out, b_lse
 

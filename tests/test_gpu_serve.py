@@ -199,8 +199,8 @@ class Batch:
                     used[at] = see[j]
             w = torch.from_numpy(~used)
             for x in (k, v):
-                xb, bb = x.view(torch.uint8 if dtype == "e4m3" else torch.int16), \
-                    bad.view(torch.uint8 if dtype == "e4m3" else torch.int16)
+                bits = {"e4m3": torch.uint8, "bf16": torch.int16, "f32": torch.int32}[dtype]
+                xb, bb = x.view(bits), bad.view(bits)
                 xb[w] = bb
         self.kc, self.vc, self.qc = k, v, q
         if joined:    # K and V interleaved token by token, Q a view of a wider tensor
@@ -222,7 +222,7 @@ class Batch:
         self.handle = fp2.make_decode(self.q, self.cache, self.cu, self.kv_len, self.max_len, hkv,
                                       tree_mask=self.words_dev, **self.descale)
         self.scratch = fp2.alloc_scratch(fp2.fp2_decode_workspace(self.handle), "cuda")
-        self.out = torch.full((T, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        self.out = torch.full((T, hq, d), 7.0, dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
         self.lse = torch.full((hq, T), 7.0, device="cuda")
         self.ds = ds
 
@@ -240,6 +240,8 @@ class Batch:
         # e4m3: weights are f16.  bf16: two bf16 halves when no sequence has over 128 rows per KV head, else one.
         if self.dtype == "e4m3":
             return R.HALF["f16"]
+        if self.dtype == "f32":
+            return 0.0
         rows = max(self.qlens) * self.hq // self.hkv
         return R.HALF["bf16"] ** 2 if rows <= 128 else R.HALF["bf16"]
 
@@ -252,7 +254,8 @@ class Batch:
             c = slice(self.cu[r], self.cu[r + 1])
             q, k, v = self.values(r)
             o, l, mag, top = R.attend(q, k, v, self.scale, self.vis[r])
-            b_out, b_lse = R.attend_bounds(o, l, mag, top, self.d, self.lens[r], self.p_half())
+            b_out, b_lse = R.attend_bounds(o, l, mag, top, self.d, self.lens[r], self.p_half(),
+                                            "f32" if self.dtype == "f32" else "bf16")
             _within(out[c], o, b_out, f"out of sequence {r}")
             empty = ~np.isfinite(l)
             assert (lse[:, c][empty] == -np.inf).all() and (out[c].transpose(1, 0, 2)[empty] == 0).all()
@@ -277,6 +280,11 @@ TREE = [
     ("e4m3", 128, 8, 8, 0, (64, 3000, 31), (1, 64, 31), "all"),
     ("bf16", 128, 8, 2, 16, (40, 6, 0, 9), (6, 6, 0, 0), "none"),  # rows without a key, sequences without a token
     ("e4m3", 128, 8, 2, 16, (40, 5, 0, 9), (6, 5, 0, 0), "none"),
+    ("f32", 64, 8, 2, 16, (300, 1, 65, 64), (1, 1, 1, 1), None),
+    ("f32", 64, 10, 2, 0, (700, 64), (5, 33), "tree"),
+    ("f32", 64, 4, 4, 64, (9000, 3), (64, 3), "all"),
+    ("f32", 64, 4, 1, 128, (40, 6, 0, 9), (6, 6, 0, 0), "none"),
+    ("f32", 64, 16, 2, 16, (300, 64), (64, 20), "tree"),
 ]
 
 
@@ -289,8 +297,8 @@ def test_tree_attend(dtype, d, hq, hkv, page, lens, qlens, mask, holes):
 
 
 def test_tree_attend_strided_inputs_and_large_scores():
-    for dtype in ("bf16", "e4m3"):
-        b = Batch(dtype, 128, 8, 2, 16, (500, 77), (3, 1), "tree", seed=5, joined=True, gain=6.0)
+    for dtype, d in (("bf16", 128), ("e4m3", 128), ("f32", 64)):
+        b = Batch(dtype, d, 8, 2, 16, (500, 77), (3, 1), "tree", seed=5, joined=True, gain=6.0)
         b.attend()
         b.check()
 
@@ -298,8 +306,9 @@ def test_tree_attend_strided_inputs_and_large_scores():
 @pytest.mark.parametrize("qlen", [1, 40])
 def test_a_value_that_only_some_tokens_see(qlen):
     """An infinite or NaN V row of a drafted key reaches exactly the rows that see the key."""
-    for dtype, bad in (("bf16", float("inf")), ("bf16", float("nan")), ("e4m3", float("nan"))):
-        b = Batch(dtype, 128, 8, 2, 64, (200,), (qlen + 2,), "tree", seed=11)
+    for dtype, d, bad in (("bf16", 128, float("inf")), ("bf16", 128, float("nan")), ("e4m3", 128, float("nan")),
+                          ("f32", 64, float("inf"))):
+        b = Batch(dtype, d, 8, 2, 64, (200,), (qlen + 2,), "tree", seed=11)
         words = b.words.clone()
         words[:] = 1                       # every token sees drafted key 0
         words[qlen] |= 1 << (qlen + 1)     # token qlen also sees the last one
@@ -319,8 +328,8 @@ def test_a_value_that_only_some_tokens_see(qlen):
 @pytest.mark.parametrize("qlen", [1, 40])
 def test_a_value_that_is_not_finite_stays_in_its_element(qlen):
     """NaN in V of a key that every token sees: NaN there, in every token of the group's heads, and nowhere else."""
-    for dtype in ("bf16", "e4m3"):
-        b = Batch(dtype, 128, 8, 2, 64, (300,), (qlen,), None, seed=12)
+    for dtype, d in (("bf16", 128), ("e4m3", 128), ("f32", 64)):
+        b = Batch(dtype, d, 8, 2, 64, (300,), (qlen,), None, seed=12)
         page = int(b.table[0, 1])
         if dtype == "e4m3":
             b.v.view(torch.uint8)[page, 7, 1, 37] = 0xFF
@@ -386,9 +395,10 @@ def test_tree_attend_is_repeatable_and_lse_is_optional():
         assert torch.equal(first, b.out)
 
 
-def test_tree_attend_bad_lengths_and_pages():
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_tree_attend_bad_lengths_and_pages(dtype, d):
     from block_sparse_long_pooled_b200 import fp2
-    b = Batch("bf16", 128, 8, 2, 16, (100, 90, 80), (2, 2, 2), None, seed=4)
+    b = Batch(dtype, d, 8, 2, 16, (100, 90, 80), (2, 2, 2), None, seed=4)
     b.kv_len.copy_(torch.tensor([100, b.max_len + 1, 1]))   # above the bound; below its tokens
     b.attend()
     st, bits = _status(b.scratch)
@@ -408,7 +418,7 @@ def test_tree_attend_bad_lengths_and_pages():
         vis = b.vis[1].copy()
         vis[:, 32:48] = False
         want, lse, mag, top = R.attend(q, k, v, b.scale, vis)
-        _within(b.out[2:4], want, R.attend_bounds(want, lse, mag, top, 128, 90, b.p_half())[0], "the other pages")
+        _within(b.out[2:4], want, R.attend_bounds(want, lse, mag, top, d, 90, b.p_half(), dtype)[0], "the other pages")
         b.table_dev[1, 2] = keep
     b.attend()
     b.check()

@@ -131,7 +131,7 @@ def _decode(n=2, qlen=3, hq=4, hkv=2, d=128, dtype="bf16", page=16, most=100, pa
     (dict(max_kv_len=113), INV),                              # more pages than the table has
     (dict(paged=False, max_kv_len=101), INV), (dict(paged=False, num_outer=1), INV),
     (dict(page=24), UNS), (dict(page=8), UNS), (dict(rows=0), INV), (dict(num_outer=0), INV),
-    (dict(num_q_heads=3), INV), (dict(num_q_heads=66), UNS), (dict(head_dim=96), UNS), (dict(dtype="f32", d=64), UNS),
+    (dict(num_q_heads=3), INV), (dict(num_q_heads=66), UNS), (dict(head_dim=96), UNS), (dict(dtype="f32", d=128), UNS),
     (dict(dtype="e4m3", d=64), UNS), (dict(softmax_scale=-1.0), INV), (dict(k_descale=0.0), INV), (dict(q=None), INV),
     (dict(kv_len=None), INV), (dict(k=None), INV), (dict(stride_tok=252), INV), (dict(stride_outer=4095), INV),
     (dict(q_stride_tok=500), INV), (dict(num_seqs=0), UNS), (dict(num_seqs=513), UNS), (dict(cu_seqlens_q_host=None), INV),
