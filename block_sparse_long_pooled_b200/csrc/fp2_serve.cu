@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -39,7 +40,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 int elt_bytes(fp2_dtype t) { return t == FP2_F32 ? 4 : (t == FP2_BF16 ? 2 : 1); }
-bool positive(float x) { return x > 0.f && std::isfinite(x); }
+bool positive(float x) { return x >= FLT_MIN && std::isfinite(x); }  // (1 / x is finite)
 
 int num_sms() {
   int dev = 0, n = 148;
@@ -62,6 +63,7 @@ fp2_status clear_status(void* scratch, cudaStream_t st) {
 fp2_status check_cache(const fp2_cache& c, int num_seqs, int64_t max_len, bool need_v) {
   if (c.dtype != FP2_F32 && c.dtype != FP2_BF16 && c.dtype != FP2_E4M3) return invalid("unknown cache dtype");
   if (c.num_kv_heads <= 0) return invalid("num_kv_heads must be positive");
+  if (c.num_kv_heads > 65536) return unsupported("more than 65536 heads");
   if (c.head_dim != 64 && c.head_dim != 128) return unsupported("head_dim must be 64 or 128");
   if (c.dtype == FP2_F32 && c.head_dim != 64) return unsupported("an F32 cache needs head_dim 64");
   if (c.dtype == FP2_E4M3 && c.head_dim != 128) return unsupported("an E4M3 cache needs head_dim 128");
@@ -106,7 +108,7 @@ fp2_status check_rotation(const fp2_rotation* p) {
   if ((p->q_norm != nullptr || p->k_norm != nullptr) && (!(p->norm_eps >= 0.f) || !std::isfinite(p->norm_eps)))
     return invalid("norm_eps must be finite and >= 0");
   if (!positive(p->q_descale) || !positive(p->k_descale) || !positive(p->v_descale))
-    return invalid("descale factors must be finite and > 0");
+    return invalid("descale factors must be finite, normal and > 0");
   if (p->out_dtype != FP2_E4M3 && (p->q_descale != 1.f || p->k_descale != 1.f || p->v_descale != 1.f))
     return invalid("descale factors other than 1 need an E4M3 output");
   if (p->rotary_dim > 0) {
@@ -188,7 +190,7 @@ struct DecodeCtx {
   bool f32 = false, few = true;         // which tree attention kernel
   int part_rows = 16, groups_tree = 1, groups_mass = 1;
   size_t off_desc = 0, off_ml = 0, off_o = 0, bytes = 0;
-  float scale = 0.f;
+  float scale_log2 = 0.f;               // of a score of stored values, in powers of two
 };
 
 int groups_for(const fp2_decode* p, int G, int tile, int rows_per_tile, int least_tiles, int ctas) {
@@ -217,7 +219,7 @@ fp2_status validate(const fp2_decode* p, bool need_v, DecodeCtx& c) {
   if (!(p->softmax_scale >= 0.f) || !std::isfinite(p->softmax_scale))
     return invalid("softmax_scale must be finite and >= 0");
   if (!positive(p->q_descale) || !positive(p->k_descale) || !positive(p->v_descale))
-    return invalid("descale factors must be finite and > 0");
+    return invalid("descale factors must be finite, normal and > 0");
   if (p->cu_seqlens_q_host[0] != 0) return invalid("cu_seqlens must start at 0");
   int most = 0;
   for (int r = 0; r < p->num_seqs; ++r) {
@@ -230,7 +232,13 @@ fp2_status validate(const fp2_decode* p, bool need_v, DecodeCtx& c) {
   c.T = p->cu_seqlens_q_host[p->num_seqs];
   c.max_rows = most * c.G;
   const int D = p->cache.head_dim;
-  c.scale = p->softmax_scale > 0.f ? p->softmax_scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
+  const float scale =
+      p->softmax_scale > 0.f ? p->softmax_scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
+  c.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 *
+                                    static_cast<double>(p->q_descale) * static_cast<double>(p->k_descale));
+  // (a product that is zero would make the scores of keys that no one sees, -infinity, NaN)
+  if (!(c.scale_log2 >= FLT_MIN) || !std::isfinite(c.scale_log2) || !std::isfinite(p->v_descale * 256.f))
+    return invalid("softmax_scale * q_descale * k_descale must be a normal fp32 number, v_descale below 2^120");
   if (p->kv_len == nullptr || !aligned4(p->kv_len)) return invalid("kv_len must be a 4-byte aligned pointer");
   if (c.T > 0) {
     if (p->q == nullptr || !aligned16(p->q)) return invalid("q must be a 16-byte aligned pointer");
@@ -291,12 +299,15 @@ fp2_status encode_q(CUtensorMap* m, const fp2_decode* p, int T, int G, int token
   const int elt = elt_bytes(c.dtype);
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(p->num_q_heads),
                               static_cast<cuuint64_t>(T)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.head_dim) * elt, static_cast<cuuint64_t>(p->q_stride_tok) * elt};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.head_dim) * elt,
+                                 static_cast<cuuint64_t>(p->q_stride_tok) * elt};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(G),
+                             static_cast<cuuint32_t>(tokens)};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUresult r = fn(m, c.dtype == FP2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                         const_cast<void*>(p->q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FP2_OK : fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }
 
@@ -327,8 +338,7 @@ fp2_status fill_decode(const fp2_decode* p, const DecodeCtx& c, void* scratch, f
   a.Hkv = p->cache.num_kv_heads;
   a.G = c.G;
   a.T = c.T;
-  a.scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634 *
-                                    static_cast<double>(p->q_descale) * static_cast<double>(p->k_descale));
+  a.scale_log2 = c.scale_log2;
   a.v_descale = p->v_descale;
   a.scratch = static_cast<uint32_t*>(scratch);
   a.wait_limit_ns = fp2_internal::wait_limit_ns();

@@ -525,6 +525,13 @@ def _expect(t, dtype, shape, what: str):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
+def _int32(x, what: str) -> int:
+    """x, which a C int holds (ctypes would cut off what does not fit)."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{what} out of range")
+    return x
+
+
 def _stored_like(a, b) -> bool:
     return _dtype_code(a) == _dtype_code(b)
 
@@ -638,6 +645,9 @@ def make_rotate(q, k, v, positions, rope: Optional[Rope], q_out, k_out, v_out, s
 def fp2_rotate(rotation: Rotation, status_dev=None, stream=None):
     """Head norms, rotary positions and cache append (include/fp2.h).  status_dev: optional int32/uint32
     device word that FP2_DEV_* bits are OR-ed into."""
+    if status_dev is not None and (status_dev.element_size() != 4 or status_dev.numel() < 1 or
+                                   status_dev.get_device() != rotation.index):
+        raise ValueError(f"status_dev must be a 4-byte word on {rotation.device}")
     rotation.call(rotation.lib.fp2_rotate, (None if status_dev is None else status_dev.data_ptr(),), stream)
 
 
@@ -667,7 +677,7 @@ def make_decode(q, cache: Cache, cu_seqlens, kv_len, max_kv_len: int, num_kv_hea
     s.q_stride_tok = q.stride(0) if q.shape[0] > 1 else q.shape[1] * q.shape[2]
     s.q_descale, s.k_descale, s.v_descale, s.softmax_scale = q_descale, k_descale, v_descale, softmax_scale
     s.cache = c
-    s.kv_len, s.max_kv_len, s.tree_mask = _ptr(kv_len), max_kv_len, _ptr(tree_mask)
+    s.kv_len, s.max_kv_len, s.tree_mask = _ptr(kv_len), _int32(max_kv_len, "max_kv_len"), _ptr(tree_mask)
     return Decode(s, (q, kv_len, tree_mask, *cache.keep), (cu,))
 
 
@@ -718,8 +728,8 @@ def make_evict(cache: Cache, kv_len, max_kv_len: int, mass, budget: int, sink: i
     _expect(kv_len_out, torch.int32, (n,), "kv_len_out")
     s = fp2_eviction()
     s.num_seqs, s.src, s.dst = n, c, cache_out.struct
-    s.kv_len, s.max_kv_len, s.mass, s.mass_stride = _ptr(kv_len), max_kv_len, _ptr(mass), mass.shape[-1]
-    s.budget, s.sink, s.window = budget, sink, window
+    s.kv_len, s.max_kv_len, s.mass, s.mass_stride = _ptr(kv_len), _int32(max_kv_len, "max_kv_len"), _ptr(mass), mass.shape[-1]
+    s.budget, s.sink, s.window = _int32(budget, "budget"), _int32(sink, "sink"), _int32(window, "window")
     s.mass_out, s.kept, s.kv_len_out = _ptr(mass_out), _ptr(kept), _ptr(kv_len_out)
     return Eviction(s, (kv_len, mass, mass_out, kept, kv_len_out, *cache.keep, *cache_out.keep))
 

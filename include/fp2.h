@@ -256,7 +256,7 @@ typedef struct {
   void* k;
   void* v;
   fp2_dtype dtype;
-  int32_t num_kv_heads, head_dim;
+  int32_t num_kv_heads, head_dim;    /* d: BF16 64 or 128, E4M3 128, F32 64 */
   int64_t stride_tok;                /* elements between tokens (>= Hkv*d) */
   int64_t stride_outer;              /* elements between pages or sequences (>= rows*stride_tok) */
   int32_t num_outer, rows;           /* pages or sequences; tokens in each (paged: a power of two >= 16) */
@@ -322,8 +322,8 @@ typedef struct {
 FP2_API fp2_status fp2_decode_workspace(const fp2_decode* decode, size_t* scratch_bytes);
 
 /* Tree attention (one token per sequence: a plain decode step).
- * out: [T, Hq, d] bf16 (f32 over an F32 cache), 16-byte aligned; lse: [Hq, T] f32 natural-log normaliser, or NULL.  A token
- * that sees no key gets zeros and -infinity.  Keys that a token does not see have no influence on
+ * out: [T, Hq, d] bf16 (f32 over an F32 cache), 16-byte aligned; lse: [Hq, T] f32 natural-log
+ * normaliser, or NULL.  A token that sees no key gets zeros and -infinity.  Keys that a token does not see have no influence on
  * it, whatever their values (NaN included); an infinite or NaN value of a key that it does see makes that
  * element infinite or NaN. */
 FP2_API fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void* scratch,

@@ -483,9 +483,10 @@ def test_key_mass(dtype, d, hq, hkv, page, lens, qlens, mask, in_place):
         _within(got[r, :, :lens[r]], keep + new, bound + 3 * R.U * (np.abs(keep) + new) + 1e-37, f"mass of sequence {r}")
 
 
-def test_key_mass_without_any_token_decays():
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_key_mass_without_any_token_decays(dtype, d):
     from block_sparse_long_pooled_b200 import fp2
-    b = Batch("bf16", 128, 8, 2, 16, (200, 0, 33), (0, 0, 0), None, seed=13)
+    b = Batch(dtype, d, 8, 2, 16, (200, 0, 33), (0, 0, 0), None, seed=13)
     mass = torch.rand((3, 2, b.max_len), generator=_gen(1)).cuda()
     out = torch.full_like(mass, -1.0)
     fp2.fp2_key_mass(b.handle, b.lse, mass, out, b.scratch, decay=0.5)

@@ -133,6 +133,8 @@ def _decode(n=2, qlen=3, hq=4, hkv=2, d=128, dtype="bf16", page=16, most=100, pa
     (dict(page=24), UNS), (dict(page=8), UNS), (dict(rows=0), INV), (dict(num_outer=0), INV),
     (dict(num_q_heads=3), INV), (dict(num_q_heads=66), UNS), (dict(head_dim=96), UNS), (dict(dtype="f32", d=128), UNS),
     (dict(dtype="e4m3", d=64), UNS), (dict(softmax_scale=-1.0), INV), (dict(k_descale=0.0), INV), (dict(q=None), INV),
+    (dict(softmax_scale=1e-39), INV), (dict(softmax_scale=1e38, q_descale=100.0), INV), (dict(v_descale=3e37), INV),
+    (dict(num_kv_heads=65537, num_q_heads=65537), UNS),
     (dict(kv_len=None), INV), (dict(k=None), INV), (dict(stride_tok=252), INV), (dict(stride_outer=4095), INV),
     (dict(q_stride_tok=500), INV), (dict(num_seqs=0), UNS), (dict(num_seqs=513), UNS), (dict(cu_seqlens_q_host=None), INV),
 ])
@@ -141,6 +143,13 @@ def test_decode_refusals(kw, code):
     with pytest.raises(fp2.FP2Error) as e:
         fp2.fp2_decode_workspace(h)
     assert e.value.status == code and fp2.fp2_last_error()
+
+
+def test_sizes_that_a_c_int_cannot_hold():
+    with pytest.raises(ValueError):
+        fp2.make_decode(torch.zeros((1, 4, 64), dtype=torch.bfloat16),
+                        fp2.make_cache(torch.zeros((1, 50, 2, 64), dtype=torch.bfloat16)), [0, 1],
+                        torch.zeros(1, dtype=torch.int32), 2 ** 32 + 50)
 
 
 def test_decode_calls_check_scratch_and_outputs():
