@@ -378,6 +378,7 @@ fp2_status fill_evict(const fp2_eviction* p, fp2::EvictArgs& a, int& ranks, size
   if (p->max_kv_len > FP2_MAX_CACHE_LEN) return unsupported("max_kv_len above FP2_MAX_CACHE_LEN");
   if (p->budget < 1 || p->sink < 0 || p->window < 0 || static_cast<int64_t>(p->sink) + p->window > p->budget)
     return invalid("budget must be >= 1, sink and window >= 0 and sink + window <= budget");
+  if (p->budget > FP2_MAX_CACHE_LEN) return unsupported("budget above FP2_MAX_CACHE_LEN");
   FP2_TRY(check_cache(p->src, p->num_seqs, p->max_kv_len, true));
   FP2_TRY(check_cache(p->dst, p->num_seqs, std::min(p->budget, p->max_kv_len), true));
   if (p->src.dtype != p->dst.dtype || p->src.num_kv_heads != p->dst.num_kv_heads || p->src.head_dim != p->dst.head_dim)

@@ -323,9 +323,9 @@ FP2_API fp2_status fp2_decode_workspace(const fp2_decode* decode, size_t* scratc
 
 /* Tree attention (one token per sequence: a plain decode step).
  * out: [T, Hq, d] bf16 (f32 over an F32 cache), 16-byte aligned; lse: [Hq, T] f32 natural-log
- * normaliser, or NULL.  A token that sees no key gets zeros and -infinity.  Keys that a token does not see have no influence on
- * it, whatever their values (NaN included); an infinite or NaN value of a key that it does see makes that
- * element infinite or NaN. */
+ * normaliser, or NULL.  A token that sees no key gets zeros and -infinity.  Keys that a token does
+ * not see have no influence on it, whatever their values (NaN included); an infinite or NaN value of a
+ * key that it does see makes that element infinite or NaN. */
 FP2_API fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void* scratch,
                                    size_t scratch_bytes, fp2_stream_t stream);
 
@@ -351,7 +351,7 @@ typedef struct {
   int32_t max_kv_len;                /* <= FP2_MAX_CACHE_LEN */
   const float* mass;                 /* device [num_seqs, Hkv, mass_stride] */
   int64_t mass_stride;               /* >= max_kv_len */
-  int32_t budget, sink, window;      /* budget >= 1, sink + window <= budget */
+  int32_t budget, sink, window;      /* 1 <= budget <= FP2_MAX_CACHE_LEN, sink + window <= budget */
   float* mass_out;                   /* device [num_seqs, Hkv, budget]: weights of the kept keys, then 0 */
   int32_t* kept;                     /* device [num_seqs, Hkv, budget]: their old indexes, then -1 */
   int32_t* kv_len_out;               /* device [num_seqs]: N; not kv_len itself */

@@ -232,6 +232,14 @@ def test_evict_refusals(kw, code):
     assert e.value.status == code and fp2.fp2_last_error()
 
 
+def test_evict_refuses_a_budget_above_the_longest_cache():
+    h = _evict()
+    h.struct.budget = 524289
+    with pytest.raises(fp2.FP2Error) as e:
+        fp2.fp2_evict_workspace(h)
+    assert e.value.status == UNS
+
+
 def test_evict_refuses_overlap_and_small_scratch():
     h = _evict()
     assert fp2.fp2_evict_workspace(h) > 0
