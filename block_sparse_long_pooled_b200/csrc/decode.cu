@@ -136,7 +136,7 @@ struct Tree {
   static constexpr float P_BIAS = F16 ? 8.f : 0.f;
 };
 
-template <int DT, int D>
+template <int DT, int D, bool SMALL>
 __global__ void __launch_bounds__(Tree<DT, D>::THREADS, 2)
     tree_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P) {
   using C = Tree<DT, D>;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(Tree<DT, D>::THREADS, 2)
 
   if (warp == C::CONSUMERS / 32) {
     // ---------------- producer
-    Producer<C::TILE, C::ELT, D> load;
+    Producer<C::TILE, C::ELT, D, SMALL> load;
     int s = 0, it = 0;
     for (long long u = u0; u < u1;) {
       const Piece p = piece_at<C::TILE>(pre, len, P.num_seqs, u, u1);
@@ -577,7 +577,7 @@ template <int DT, int D>
 cudaError_t run_tree(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
   using C = Tree<DT, D>;
   static_assert(C::STAGES >= 2, "tiles must fit twice");
-  const auto kernel = tree_kernel<DT, D>;
+  const auto kernel = a.box_rows < 64 ? tree_kernel<DT, D, true> : tree_kernel<DT, D, false>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_chained(kernel, dim3(a.groups * a.Hkv), C::THREADS, C::SMEM, stream, 1, a, P);

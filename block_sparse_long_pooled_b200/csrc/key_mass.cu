@@ -92,7 +92,7 @@ FP2_DEVICE void ld32_now(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 
-template <int DT, int D>
+template <int DT, int D, bool SMALL>
 __global__ void __launch_bounds__(kMassThreads, 1)
     mass_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P) {
   using C = Mass<DT, D>;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 
   if (warp == 8) {
     // ---------------------------------------------------------------- producer
-    Producer<C::TILE, C::ELT, D> load;
+    Producer<C::TILE, C::ELT, D, SMALL> load;
     int it = 0;
     bool alive = true;
     for (long long u = u0; u < u1 && alive;) {
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 template <int DT, int D>
 cudaError_t run_mass(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
   using C = Mass<DT, D>;
-  const auto kernel = mass_kernel<DT, D>;
+  const auto kernel = a.box_rows < 64 ? mass_kernel<DT, D, true> : mass_kernel<DT, D, false>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_chained(kernel, dim3(a.groups * a.Hkv), kMassThreads, C::SMEM, stream, 1, a, P);

@@ -227,7 +227,7 @@ __device__ __noinline__ void add_cleared(const DecodeArgs& a, int r, int g, int 
   }
 }
 
-template <int DT, int D, bool SPLIT>
+template <int DT, int D, bool SPLIT, bool SMALL>
 __global__ void __launch_bounds__(kWideThreads, 1)
     tree_wide_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P) {
   using C = Wide<DT, D, SPLIT>;
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint64_t* full = is_k ? k_full : v_full;
       uint64_t* empty = is_k ? k_empty : v_empty;
       const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V);
-      Producer<C::TILE, C::ELT, D> load;
+      Producer<C::TILE, C::ELT, D, SMALL> load;
       int it = 0;
       bool alive = true;
       for (long long u = u0; u < u1 && alive;) {
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 template <int DT, int D, bool SPLIT>
 cudaError_t run(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
   using C = Wide<DT, D, SPLIT>;
-  const auto kernel = tree_wide_kernel<DT, D, SPLIT>;
+  const auto kernel = a.box_rows < 64 ? tree_wide_kernel<DT, D, SPLIT, true> : tree_wide_kernel<DT, D, SPLIT, false>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_chained(kernel, dim3(a.groups * a.Hkv), kWideThreads, C::SMEM, stream, 1, a, P);
