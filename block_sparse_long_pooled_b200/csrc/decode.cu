@@ -483,9 +483,10 @@ __global__ void __launch_bounds__(Tree<DT, D>::THREADS, 2)
   store_status(a, &status_word);
 }
 
-// Joins the pieces of an item that several groups worked on, in group order: one warp per row,
-// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-template <int D>
+// Joins the pieces of an item that several groups worked on, in group order,
+// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i: WARPS warps per row, each an equal run of the pieces; the
+// first then adds up what the others have.
+template <int D, int WARPS>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeArgs a,
                                                    const __grid_constant__ DecodePlan P) {
   grid_launch_next();
@@ -493,7 +494,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
   const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
   const int4 d = a.desc[grp];
   if (d.x < 0) return;
-  const int rr = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  constexpr int ROWS = 4 / WARPS;  // of a block
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = blockIdx.y * ROWS + warp / WARPS, part = warp % WARPS;
   const int t0 = P.q_off[d.y], rows = (P.q_off[d.y + 1] - t0) * a.G, m = d.z * a.part_rows + rr;
   if (m >= rows) return;
   const auto at = [&](int i) {  // row of piece i in the partial buffers
@@ -506,8 +509,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
   // Up to 32 pieces at a time, lane i with the statistics of piece i; all their rows are on their way
   // together, 16 at a time.
-  for (int i0 = 0; i0 < d.w; i0 += 32) {
-    const int n = min(32, d.w - i0);
+  const int first = d.w * part / WARPS, last = d.w * (part + 1) / WARPS;
+  for (int i0 = first; i0 < last; i0 += 32) {
+    const int n = min(32, last - i0);
     const float2 ml = lane < n ? a.part_ml[at(i0 + lane)] : make_float2(neg_inf(), 0.f);
     float x[16][V];
     const auto fetch = [&](int i1) {
@@ -555,6 +559,27 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
       }
     }
   }
+  if constexpr (WARPS > 1) {
+    __shared__ float sums[WARPS][D], tops[WARPS], totals[WARPS];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sums[part][lane * V + e] = acc[e];
+    if (lane == 0) tops[part] = top, totals[part] = total;
+    __syncthreads();  // (a block has one row: all its warps come here or none)
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, tops[w]);
+    total = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (totals[w] == 0.f) continue;
+      const float f = fast_exp2(tops[w] - top);
+      total += totals[w] * f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += sums[w][lane * V + e] * f;
+    }
+  }
   const int tok = m / a.G, h = g * a.G + (m - tok * a.G);
   const int64_t row = static_cast<int64_t>(t0) + tok;
   const float f = total == 0.f ? 0.f : a.v_descale / total;
@@ -594,8 +619,10 @@ cudaError_t launch_tree_few(int dtype, int D, const DecodeArgs& a, const DecodeP
 
 cudaError_t launch_tree_join(int D, int max_rows, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
   const int rows = max_rows < a.part_rows ? max_rows : a.part_rows;
-  return launch_chained(D == 128 ? join_kernel<128> : join_kernel<64>, dim3(a.groups * a.Hkv, (rows + 3) / 4), 128, 0,
-                        stream, 1, a, P);
+  const dim3 grid(a.groups * a.Hkv, a.join_warps == 4 ? rows : (rows + 3) / 4);
+  const auto kernel = D == 128 ? (a.join_warps == 4 ? join_kernel<128, 4> : join_kernel<128, 1>)
+                               : (a.join_warps == 4 ? join_kernel<64, 4> : join_kernel<64, 1>);
+  return launch_chained(kernel, grid, 128, 0, stream, 1, a, P);
 }
 
 }  // namespace fp2

@@ -186,7 +186,7 @@ fp2_status run_rotate(const fp2_rotation* p, uint32_t* status_dev, cudaStream_t 
 // ------------------------------------------------------------------ decode
 
 struct DecodeCtx {
-  int G = 0, T = 0, max_rows = 0;
+  int G = 0, T = 0, max_rows = 0, items = 1;
   bool f32 = false, few = true;         // which tree attention kernel
   int part_rows = 16, groups_tree = 1, groups_mass = 1;
   size_t off_desc = 0, off_ml = 0, off_o = 0, bytes = 0;
@@ -253,6 +253,9 @@ fp2_status validate(const fp2_decode* p, bool need_v, DecodeCtx& c) {
   c.f32 = p->cache.dtype == FP2_F32;
   c.few = c.f32 || c.max_rows <= fp2::kFewRows;
   c.part_rows = c.few ? fp2::kFewRows : (c.max_rows <= 128 ? 128 : 256);
+  c.items = 0;
+  for (int r = 0; r < p->num_seqs; ++r)
+    c.items += ((p->cu_seqlens_q_host[r + 1] - p->cu_seqlens_q_host[r]) * c.G + c.part_rows - 1) / c.part_rows;
   c.groups_tree = c.few ? groups_for(p, c.G, fp2::kFewTile, fp2::kFewRows, 0, sms * (c.f32 && c.max_rows <= 4 ? 3 : 2))
                         : groups_for(p, c.G, fp2::kWideTile, 128, 0, sms);
   c.groups_mass = c.f32 ? groups_for(p, c.G, fp2::kMassTile, FP2_MAX_DRAFT * c.G, 1, sms * 4)
@@ -471,6 +474,10 @@ fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void
   a.part_o = reinterpret_cast<float*>(base + c.off_o);
   a.part_rows = c.part_rows;
   a.out_f32 = c.f32 ? 1 : 0;
+  // Few items over many groups have many pieces each: one request of 20K e4m3 keys, 44 rows of one KV head, 148
+  // pieces, took 27 us with a warp per row and 22 with four.  With 37 pieces (80K keys, 84 rows, 4 KV heads) the
+  // blocks that find nothing to join cost more: 39 and 44 us.
+  a.join_warps = c.groups_tree >= 64 * c.items ? 4 : 1;
   if (!c.few && decode->cache.dtype == FP2_E4M3) a.v_descale *= 256.f;  // tree_wide.cu works on V * 2^-8
   const int D = decode->cache.head_dim;
   FP2_TRY(launched(c.f32   ? fp2::launch_tree_f32(a, P, st)

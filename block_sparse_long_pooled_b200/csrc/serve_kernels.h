@@ -100,6 +100,7 @@ struct DecodeArgs {
   // tree attention
   void* out;                  // [T, Hq, d] bf16, or f32
   int out_f32;
+  int join_warps;             // warps that join one row: 1 or 4
   float* lse;                 // [Hq, T] or NULL
   int4* desc;                 // [groups] {slot of the first piece of a split item or -1, sequence, row tile, pieces}
   float2* part_ml;            // [groups * Hkv * 2][rows] running maximum (log2 units) and sum
