@@ -13,16 +13,17 @@
 // One pass over memory: a thread owns 16 values of a head as two vectors of 8 that hold whole pairs
 // ((8c.., rot/2 + 8c..) in the half layout, 16 neighbours in the interleaved one), so no value
 // crosses threads and in-place calls are safe; d / 16 threads share a head's norm by shuffles.  A
-// warp walks the heads of one token, first Q's, then K's, then V's.  Bytes should bound it, but at 335
+// warp walks the heads of a token, first Q's, then K's, then V's.  Bytes should bound it, but at 335
 // million values the instructions count as much: norm weight, cosine and sine are multiplied once per
 // token into four factors a pair, so that a head costs a thread two products, two fused ones and the
 // norm's factor for each pair, in packed fp32 pairs; and the values come four steps ahead through shared
-// memory, as loads into registers left the SM waiting (250 and 220 us).  With few tokens the heads are
-// spread over more warps instead (run_rotate).
+// memory, as loads into registers left the SM waiting (250 and 220 us).  With many tokens, or few heads,
+// each group of d / 16 lanes has a token of its own, so that a warp's work on one token (angles, factors,
+// addresses) serves two to eight; with few tokens the heads are spread over more warps instead (run_rotate).
 //
-// Measured: 64K tokens of 32 + 4 + 4 heads, norms, bf16 to e4m3 pages: 196 us, 5.1 TB/s (154 us at the
-// copy's rate); some 2,500 warp instructions a token issue in three quarters of the cycles.  Eight tokens:
-// 2.9 us in a graph, 4 to 5 us by call, which is the host's time.
+// Measured: 64K tokens of 32 + 4 + 4 heads, norms, bf16 to e4m3 pages: 166 us, 6.1 TB/s (154 us at the
+// copy's rate; 178 us with a token a warp).  Eight tokens: 2.9 us in a graph, 4 to 5 us by call, which is the
+// host's time.
 #include "fp2_device.cuh"
 #include "serve_kernels.h"
 
@@ -32,8 +33,9 @@ namespace {
 
 constexpr int kRotThreads = 128;
 // Blocks per SM that the registers are cut for: 7 of bf16 (72 registers; 6 or 8 were 1 and 4 % slower on the
-// prompt below), 4 of f32 (with 5 an odd chunk of 1537 tokens took 7.2 us instead of 6.2).
-constexpr int blocks_per_sm(int din) { return din == 0 ? 4 : 7; }
+// prompt below), 6 with several tokens a warp, whose factors take more shared memory (5 and 7: 4 and 2 % slower),
+// 4 of f32 (with 5 an odd chunk of 1537 tokens took 7.2 us instead of 6.2).
+constexpr int blocks_per_sm(int din, bool many) { return din == 0 ? 4 : (many ? 6 : 7); }
 
 // Eight values from four words of two bf16, or eight floats.
 template <int DIN>
@@ -94,20 +96,27 @@ FP2_DEVICE float4 lds_f4(uint32_t addr) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-// DIN / DOUT: 0 f32, 1 bf16, 2 e4m3.
-template <int DIN, int DOUT, int D, bool INTER>
-__global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel(const __grid_constant__ RotateArgs a) {
+// DIN / DOUT: 0 f32, 1 bf16, 2 e4m3.  MANY: a warp has several tokens, a group of D / 16 lanes each; else one, and
+// its groups of lanes have one head each.
+template <int DIN, int DOUT, int D, bool INTER, bool MANY>
+__global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN, MANY)) rotate_kernel(const __grid_constant__ RotateArgs a) {
   grid_launch_next();
   grid_wait();
   constexpr int TPH = D / 16;                          // threads per head
-  constexpr int HPW = 32 / TPH;                        // heads per warp step
-  // A warp's four factors a pair: in shared memory, as 32 registers more would halve the warps per SM.
-  __shared__ __align__(16) float factors[kRotThreads / 32][4][2][TPH][4];
+  constexpr int GROUPS = 32 / TPH;                     // of lanes
+  constexpr int HPW = MANY ? 1 : GROUPS;               // heads of a token per step
+  constexpr int FL = MANY ? 32 : TPH;                  // lanes with factors of their own
+  // Four factors a pair: in shared memory, as 32 registers more would halve the warps per SM.
+  __shared__ __align__(16) float factors[kRotThreads / 32][4][2][FL][4];
   constexpr int EIN = DIN == 0 ? 4 : 2, EOUT = DOUT == 0 ? 4 : (DOUT == 1 ? 2 : 1);
   const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRotThreads / 32) + (threadIdx.x >> 5);
-  if (t >= a.tokens) return;
-  const int p = lane % TPH;
+  const int p = lane % TPH, group = lane / TPH;
+  const int head0 = MANY ? 0 : group;                  // of this lane in a step
+  int64_t t = static_cast<int64_t>(blockIdx.x) * (kRotThreads / 32) + (threadIdx.x >> 5);
+  if constexpr (MANY) t = t * GROUPS + group;
+  const bool mine = t < a.tokens;
+  if (!__any_sync(0xFFFFFFFFu, mine)) return;
+  if (!mine) t = a.tokens - 1;                         // (such lanes load what another does and store nothing)
   const int half = a.rot >> 1;
   // The two vectors of 8 values: whole pairs of the rotated part, or 16 values of the rest.
   const bool rotated = 16 * p < a.rot;
@@ -135,7 +144,7 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
         const int base = which == 0 ? 0 : (which == 1 ? sq : sq + sk);
         ask_end = which == 0 ? sq : (which == 1 ? sq + sk : sq + sk + sv);
         ask_heads = which == 0 ? a.Hq : a.Hkv;
-        ask_head = (ask - base) * HPW + lane / TPH;
+        ask_head = (ask - base) * HPW + head0;
         const char* at = static_cast<const char*>(which == 0 ? a.q : (which == 1 ? a.k : a.v)) +
                          (t * (which == 0 ? a.q_stride : (which == 1 ? a.k_stride : a.v_stride)) +
                           static_cast<int64_t>(ask_head) * D) * EIN;
@@ -170,14 +179,14 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
 
   // The TPH lanes of every head need the same 8 pairs' cosines and sines: each of the HPW groups of
   // lanes works out 8 / HPW of them and the others take them over.
-  constexpr int MINE = 8 / HPW > 0 ? 8 / HPW : 1;
+  constexpr int MINE = 8 / HPW;
   float cs[8], sn[8];
   if (begin < sq + sk && a.rot > 0) {
     const int64_t pos = a.positions[t];
     float cm[MINE], sm[MINE];
 #pragma unroll
     for (int m = 0; m < MINE; ++m) {
-      const int i = (lane / TPH) * MINE + m;
+      const int i = head0 * MINE + m;
       const uint64_t phase = rotated ? a.phase[8 * p + i] : 0;
       const uint32_t turn = static_cast<uint32_t>((static_cast<uint64_t>(pos) * phase) >> 32);
       const uint32_t quarter = (turn + 0x20000000u) >> 30;
@@ -190,16 +199,16 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      cs[i] = __shfl_sync(0xFFFFFFFFu, cm[i % MINE], (i / MINE) * TPH + p);
-      sn[i] = __shfl_sync(0xFFFFFFFFu, sm[i % MINE], (i / MINE) * TPH + p);
+      cs[i] = MANY ? cm[i % MINE] : __shfl_sync(0xFFFFFFFFu, cm[i % MINE], (i / MINE) * TPH + p);
+      sn[i] = MANY ? sm[i % MINE] : __shfl_sync(0xFFFFFFFFu, sm[i % MINE], (i / MINE) * TPH + p);
     }
   }
   int64_t row = t;
-  bool put = true;
+  bool put = mine;
   if (a.slots != nullptr && end > sq) {
     row = a.slots[t];
-    put = row >= 0 && row < a.num_slots;
-    if (row >= a.num_slots && a.status != nullptr && lane == 0 && end == sq + sk + sv)
+    put = mine && row >= 0 && row < a.num_slots;
+    if (row >= a.num_slots && a.status != nullptr && lane == TPH * group * MANY && mine && end == sq + sk + sv)
       set_status(a.status, FP2_DEV_SLOT_OOB);
   }
 
@@ -208,13 +217,15 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
     const int base = which == 0 ? 0 : (which == 1 ? sq : sq + sk), steps = which == 0 ? sq : (which == 1 ? sk : sv);
     const int heads = which == 0 ? a.Hq : (which == 1 ? a.Hkv : a.Hv);
     const int s0 = max(begin - base, 0), s1 = min(end - base, steps);
-    if (s0 >= s1 || (which > 0 && !put)) continue;  // (K and V without a place are the last steps)
+    // (K and V without a place are the last steps)
+    if (s0 >= s1 || (which > 0 && !__any_sync(0xFFFFFFFFu, put))) continue;
+    const bool store = which > 0 ? put : mine;
     char* dst = static_cast<char*>(which == 0 ? a.q_out : (which == 1 ? a.k_out : a.v_out)) +
                 (which == 0 ? t * a.q_out_stride : row * a.kv_out_stride) * EOUT;
     const float inv = DOUT == 2 ? (which == 0 ? a.q_inv : (which == 1 ? a.k_inv : a.v_inv)) : 1.f;
     if (which == 2) {
       // V passes through: 16 neighbours a thread, whatever Q's layout.
-      int h = s0 * HPW + lane / TPH;
+      int h = s0 * HPW + head0;
       char* to = dst + (static_cast<int64_t>(h) * D + 16 * p) * EOUT;
 #pragma unroll 1
       for (int s = s0; s < s1; ++s) {
@@ -225,7 +236,7 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] *= inv, y[i] *= inv;
         }
-        if (h < heads) {
+        if (h < heads && store) {
           store8<DOUT>(to, x);
           store8<DOUT>(to + 8 * EOUT, y);
         }
@@ -266,22 +277,23 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
     }
 
     __syncwarp();
-    float (*fac)[2][TPH][4] = factors[threadIdx.x >> 5];
-    if (lane < TPH) {
+    float (*fac)[2][FL][4] = factors[threadIdx.x >> 5];
+    const int fl = MANY ? lane : p;
+    if (lane < FL) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        *reinterpret_cast<float4*>(fac[0][q][p]) = make_float4(f1[4 * q], f1[4 * q + 1], f1[4 * q + 2], f1[4 * q + 3]);
-        *reinterpret_cast<float4*>(fac[1][q][p]) = make_float4(f2[4 * q], f2[4 * q + 1], f2[4 * q + 2], f2[4 * q + 3]);
-        *reinterpret_cast<float4*>(fac[2][q][p]) = make_float4(f3[4 * q], f3[4 * q + 1], f3[4 * q + 2], f3[4 * q + 3]);
-        *reinterpret_cast<float4*>(fac[3][q][p]) = make_float4(f4[4 * q], f4[4 * q + 1], f4[4 * q + 2], f4[4 * q + 3]);
+        *reinterpret_cast<float4*>(fac[0][q][fl]) = make_float4(f1[4 * q], f1[4 * q + 1], f1[4 * q + 2], f1[4 * q + 3]);
+        *reinterpret_cast<float4*>(fac[1][q][fl]) = make_float4(f2[4 * q], f2[4 * q + 1], f2[4 * q + 2], f2[4 * q + 3]);
+        *reinterpret_cast<float4*>(fac[2][q][fl]) = make_float4(f3[4 * q], f3[4 * q + 1], f3[4 * q + 2], f3[4 * q + 3]);
+        *reinterpret_cast<float4*>(fac[3][q][fl]) = make_float4(f4[4 * q], f4[4 * q + 1], f4[4 * q + 2], f4[4 * q + 3]);
       }
     }
     __syncwarp();
 
-    int h = s0 * HPW + lane / TPH;
+    int h = s0 * HPW + head0;
     char* to = dst + (static_cast<int64_t>(h) * D + e0) * EOUT;
     const int apart = (e1 - e0) * EOUT;
-    const uint32_t fac_at = smem_u32(fac[0][0][p]);
+    const uint32_t fac_at = smem_u32(fac[0][0][fl]);
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       float v0[8], v1[8], x1[8], x2[8];
@@ -313,8 +325,8 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
       const float2 r2 = make_float2(r, r);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float4 g1 = lds_f4(fac_at + q * (TPH * 16)), g3 = lds_f4(fac_at + (4 + q) * (TPH * 16));
-        const float4 g2 = lds_f4(fac_at + (2 + q) * (TPH * 16)), g4 = lds_f4(fac_at + (6 + q) * (TPH * 16));
+        const float4 g1 = lds_f4(fac_at + q * (FL * 16)), g3 = lds_f4(fac_at + (4 + q) * (FL * 16));
+        const float4 g2 = lds_f4(fac_at + (2 + q) * (FL * 16)), g4 = lds_f4(fac_at + (6 + q) * (FL * 16));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = 4 * q + 2 * e;
@@ -341,7 +353,7 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
           v1[2 * i] = x1[4 + i], v1[2 * i + 1] = x2[4 + i];
         }
       }
-      if (h < heads) {
+      if (h < heads && store) {
         store8<DOUT>(to, v0);
         store8<DOUT>(to + apart, v1);
       }
@@ -352,19 +364,32 @@ __global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN)) rotate_kernel
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+template <int DIN, int DOUT, int D, bool MANY>
+cudaError_t run_layout(RotateArgs& a, int chunks, cudaStream_t stream) {
+  constexpr int GROUPS = 32 / (D / 16), HPW = MANY ? 1 : GROUPS, PER_BLOCK = kRotThreads / 32 * (MANY ? GROUPS : 1);
+  const int steps = (a.Hq + HPW - 1) / HPW + (a.Hkv + HPW - 1) / HPW + (a.Hv + HPW - 1) / HPW;
+  if (chunks > steps) chunks = steps;
+  a.iters = (steps + chunks - 1) / chunks;
+  const dim3 grid(static_cast<unsigned>((a.tokens + PER_BLOCK - 1) / PER_BLOCK), (steps + a.iters - 1) / a.iters);
+  return launch_chained(a.interleaved ? rotate_kernel<DIN, DOUT, D, true, MANY> : rotate_kernel<DIN, DOUT, D, false, MANY>,
+                        grid, kRotThreads, 0, stream, 1, a);
+}
+
 template <int DIN, int DOUT, int D>
 cudaError_t run_rotate(RotateArgs a, cudaStream_t stream) {
-  constexpr int HPW = 32 / (D / 16);
-  const int steps = (a.Hq + HPW - 1) / HPW + (a.Hkv + HPW - 1) / HPW + (a.Hv + HPW - 1) / HPW;
+  // A warp with one token spends 1.3 ns of the GPU on every one, whatever its heads, and lanes without a head; a
+  // warp with several needs tokens enough to fill the GPU, and its loads are single heads.  Tokens 600, 2400,
+  // 9600, 40000 (us, one | several):  3 heads bf16 to bf16, d 128  5, 8, 16, 53 | 4, 5, 8, 19;  8 heads  5, 8, 16, 56 |
+  // 6, 7, 12, 36;  24 heads, d 64  4, 8, 16, 63 | 10, 10, 22, 54;  40 heads bf16 to e4m3  8, 14, 33, 111 | 15, 20, 38,
+  // 106;  48 heads bf16 to bf16, bound by its 25 KB a token  8, 16, 42, 149 | 17, 24, 52, 165.
+  constexpr int HEAD = D * ((DIN == 0 ? 4 : 2) + (DOUT == 0 ? 4 : (DOUT == 1 ? 2 : 1)));  // bytes of a head
+  const int heads = a.Hq + a.Hkv + a.Hv;
+  if (heads <= 8 ? a.tokens >= 148 * 16 : a.tokens >= 16384 && static_cast<int64_t>(heads) * HEAD < 20480)
+    return run_layout<DIN, DOUT, D, true>(a, 1, stream);
   // A warp walks all heads of its token when there are tokens enough to fill the GPU (148 SMs x 16
   // warps); below that the steps are spread over the grid's y, at the price of more sines.
   const int64_t want = (148 * 16 + a.tokens - 1) / a.tokens;
-  const int chunks = static_cast<int>(want < 1 ? 1 : (want > steps ? steps : want));
-  a.iters = (steps + chunks - 1) / chunks;
-  const dim3 grid(static_cast<unsigned>((a.tokens + kRotThreads / 32 - 1) / (kRotThreads / 32)),
-                  (steps + a.iters - 1) / a.iters);
-  return launch_chained(a.interleaved ? rotate_kernel<DIN, DOUT, D, true> : rotate_kernel<DIN, DOUT, D, false>, grid,
-                        kRotThreads, 0, stream, 1, a);
+  return run_layout<DIN, DOUT, D, false>(a, static_cast<int>(want < 1 ? 1 : want), stream);
 }
 
 }  // namespace

@@ -56,6 +56,13 @@ def _status(scratch):
     ("f32", "e4m3", 64, 48, False, False, 19, 4, 4, 16),
     ("bf16", "bf16", 128, 0, False, True, 40, 4, 2, 0),        # norms only
     ("bf16", "bf16", 128, 112, False, False, 3000, 9, 1, 64),  # warps that walk several heads
+    # so many tokens that a warp has several
+    ("bf16", "e4m3", 128, 128, False, True, 9601, 3, 1, 16),
+    ("bf16", "bf16", 128, 48, True, False, 9474, 1, 2, 0),
+    ("bf16", "bf16", 64, 64, False, True, 18949, 1, 1, 64),
+    ("f32", "f32", 64, 32, True, True, 19001, 2, 1, 0),
+    ("f32", "e4m3", 64, 64, False, False, 18947, 1, 1, 128),
+    ("bf16", "bf16", 64, 32, True, True, 16401, 8, 1, 16),
 ])
 def test_rotate(src, dst, d, rot, inter, norm, tokens, hq, hkv, page):
     from block_sparse_long_pooled_b200 import fp2
@@ -285,6 +292,10 @@ TREE = [
     ("f32", 64, 4, 4, 64, (9000, 3), (64, 3), "all"),
     ("f32", 64, 4, 1, 128, (40, 6, 0, 9), (6, 6, 0, 0), "none"),
     ("f32", 64, 16, 2, 16, (300, 64), (64, 20), "tree"),
+    # one sequence in 74 pieces or more
+    ("bf16", 64, 4, 1, 16, (20001,), (3,), "tree"),
+    ("e4m3", 128, 4, 1, 0, (12000,), (11,), "tree"),
+    ("f32", 64, 4, 1, 64, (8200,), (2,), None),
 ]
 
 
