@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const __grid_constan
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (m < rows) {
         const int tok = m / a.G, h = g * a.G + (m - tok * a.G);
-        x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (static_cast<int64_t>(t0) + tok) * a.q_stride +
+        x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                             (static_cast<int64_t>(t0) + tok) * a.q_stride +
                                              static_cast<int64_t>(h) * kD + 4 * c);
       }
       *reinterpret_cast<float4*>(&s.q[rr][4 * c]) = x;
@@ -300,8 +301,8 @@ __global__ void __launch_bounds__(kThreads) mass_f32_kernel(const __grid_constan
       for (int i = tid; i < n * (kD / 4); i += kThreads) {
         const int rr = i / (kD / 4), c = i % (kD / 4), tok = (c0 + rr) / a.G, h = g * a.G + (c0 + rr - tok * a.G);
         *reinterpret_cast<float4*>(&s.q[rr][4 * c]) = *reinterpret_cast<const float4*>(
-            static_cast<const float*>(a.q) + (static_cast<int64_t>(t0) + tok) * a.q_stride + static_cast<int64_t>(h) * kD +
-            4 * c);
+            static_cast<const float*>(a.q) + (static_cast<int64_t>(t0) + tok) * a.q_stride +
+            static_cast<int64_t>(h) * kD + 4 * c);
       }
       for (int rr = tid; rr < n; rr += kThreads) {
         const int tok = (c0 + rr) / a.G, h = g * a.G + (c0 + rr - tok * a.G);

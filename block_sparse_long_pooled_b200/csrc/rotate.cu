@@ -99,7 +99,8 @@ FP2_DEVICE float4 lds_f4(uint32_t addr) {
 // DIN / DOUT: 0 f32, 1 bf16, 2 e4m3.  MANY: a warp has several tokens, a group of D / 16 lanes each; else one, and
 // its groups of lanes have one head each.
 template <int DIN, int DOUT, int D, bool INTER, bool MANY>
-__global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN, MANY)) rotate_kernel(const __grid_constant__ RotateArgs a) {
+__global__ void __launch_bounds__(kRotThreads, blocks_per_sm(DIN, MANY))
+    rotate_kernel(const __grid_constant__ RotateArgs a) {
   grid_launch_next();
   grid_wait();
   constexpr int TPH = D / 16;                          // threads per head
@@ -371,8 +372,9 @@ cudaError_t run_layout(RotateArgs& a, int chunks, cudaStream_t stream) {
   if (chunks > steps) chunks = steps;
   a.iters = (steps + chunks - 1) / chunks;
   const dim3 grid(static_cast<unsigned>((a.tokens + PER_BLOCK - 1) / PER_BLOCK), (steps + a.iters - 1) / a.iters);
-  return launch_chained(a.interleaved ? rotate_kernel<DIN, DOUT, D, true, MANY> : rotate_kernel<DIN, DOUT, D, false, MANY>,
-                        grid, kRotThreads, 0, stream, 1, a);
+  const auto kernel =
+      a.interleaved ? rotate_kernel<DIN, DOUT, D, true, MANY> : rotate_kernel<DIN, DOUT, D, false, MANY>;
+  return launch_chained(kernel, grid, kRotThreads, 0, stream, 1, a);
 }
 
 template <int DIN, int DOUT, int D>
