@@ -46,12 +46,17 @@ struct Wide {
   static constexpr int Q_BYTES = 128 * D * ELT;   // one M tile
   static constexpr int KV_BYTES = TILE * D * ELT; // one K or V tile
   static constexpr int V16_BYTES = E4 ? TILE * D * 2 : 0;
-  static constexpr int STAGES = E4 || D == 64 ? 6 : 4;
+  // Rings.  A wait names its phase by parity alone, so whoever waits on a barrier has to have seen the phase before
+  // it end; loads land in any order, so only a waiter's own earlier waits tell it that.
+  //   K: the issuers wait.  In parity a stream meets every second tile: an even ring gives it both phases of a stage,
+  //      in an odd one the stages would belong to the streams in turn.
+  //   V: the four V warps wait, each for every fourth tile: the ring is a multiple of four, or a warp would meet a
+  //      stage in some of its phases only.  The same for the copies.
+  static constexpr int K_STAGES = E4 || D == 64 ? 6 : 4;
+  static constexpr int V_STAGES = E4 || D == 64 ? 8 : 4;
   static constexpr int COPIES = 4;                // of V in f16
-  // Even, both: in parity a stream then meets every second stage only, and each of its phases.  With an odd
-  // ring a stage would belong to the streams in turn, and a stream that waits for its next phase there would
-  // take its own last one, of the same parity, for it.
-  static_assert(STAGES % 2 == 0 && COPIES % 2 == 0, "rings of two streams");
+  static constexpr int V_WARPS = 4;
+  static_assert(K_STAGES % 2 == 0 && V_STAGES % V_WARPS == 0 && COPIES % V_WARPS == 0, "rings and their waiters");
   static constexpr int KIND_QK = E4 ? 2 : 1, UK = 32 / ELT;
   static constexpr uint32_t FMT_QK = E4 ? 0u : 1u, FMT_PV = E4 ? 0u : 1u;  // e4m3 / bf16; f16 / bf16
   static constexpr uint32_t IDESC_S = make_idesc(FMT_QK, FMT_QK, 0, 0, 128, TILE);
@@ -61,14 +66,15 @@ struct Wide {
   // and 2^(4 + LAZY) far below the largest value.
   static constexpr float P_BIAS = E4 ? 4.f : 0.f;
   static constexpr int OFF_Q = 0;                              // [2] M tiles
-  static constexpr int OFF_K = 2 * Q_BYTES;                    // [STAGES]
-  static constexpr int OFF_V = OFF_K + STAGES * KV_BYTES;      // [STAGES]
-  static constexpr int OFF_V16 = OFF_V + STAGES * KV_BYTES;    // [COPIES]
+  static constexpr int OFF_K = 2 * Q_BYTES;                    // [K_STAGES]
+  static constexpr int OFF_V = OFF_K + K_STAGES * KV_BYTES;    // [V_STAGES]
+  static constexpr int OFF_V16 = OFF_V + V_STAGES * KV_BYTES;  // [COPIES]
   static constexpr int OFF_ML = OFF_V16 + COPIES * V16_BYTES;       // [128] float2: maximum and sum of stream 1
   static constexpr int OFF_PRE = OFF_ML + 128 * 8;
   static constexpr int OFF_LEN = OFF_PRE + (FP2_MAX_SEQS + 1) * 8;
   static constexpr int OFF_BAR = (OFF_LEN + FP2_MAX_SEQS * 4 + 15) / 16 * 16;
-  static constexpr int SMEM_RAW = OFF_BAR + 512 + 1024;
+  static constexpr int BARS = 2 * K_STAGES + 3 * V_STAGES + COPIES + 16;
+  static constexpr int SMEM_RAW = OFF_BAR + BARS * 8 + 1024;
   // One CTA per SM: it holds all of TMEM.
   static constexpr int SMEM = SMEM_RAW > 116 * 1024 ? SMEM_RAW : 116 * 1024;
   static_assert(SMEM <= 226 * 1024, "shared memory");
@@ -239,22 +245,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   int* len = reinterpret_cast<int*>(smem + C::OFF_LEN);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* k_full = bars;                    // the K tile has landed
-  uint64_t* k_empty = k_full + C::STAGES;     // both streams are done with it
-  uint64_t* v_full = k_empty + C::STAGES;
-  uint64_t* v_empty = v_full + C::STAGES;     // bf16: by the MMA issuers; e4m3: by the V warps
-  uint64_t* v_ready = v_empty + C::STAGES;    // V (e4m3: copy it % COPIES) can be multiplied
-  uint64_t* v_used = v_ready + C::STAGES;     // [COPIES] e4m3: the copy is free again
+  uint64_t* k_empty = k_full + C::K_STAGES;   // both streams are done with it
+  uint64_t* v_full = k_empty + C::K_STAGES;
+  uint64_t* v_empty = v_full + C::V_STAGES;   // bf16: by the MMA issuers; e4m3: by the V warps
+  uint64_t* v_ready = v_empty + C::V_STAGES;  // V (e4m3: copy it % COPIES) can be multiplied
+  uint64_t* v_used = v_ready + C::V_STAGES;   // [COPIES] e4m3: the copy is free again
   uint64_t* q_ready = v_used + C::COPIES;     // [2] stream s may start the piece's products
   uint64_t* s_full = q_ready + 2;             // [stream][buffer], as the next two
   uint64_t* p_full = s_full + 4;
   uint64_t* pv_done = p_full + 4;
   uint64_t* all_done = pv_done + 4;           // [2]
   // Which rows of a tile hold keys: valid_v goes with the V stage.  The softmax reads valid_k later than
-  // its K stage is released: S(x - STAGES) is issued then, whose buffer the stream's tile two before had
-  // (in parity four tiles before), so everything up to tile x - STAGES - 5 has been read.
+  // its K stage is released: S(x - K_STAGES) is issued then, whose buffer the stream's tile two before had
+  // (in parity four tiles before), so everything up to tile x - K_STAGES - 5 has been read.
   constexpr int VALID = 16;
-  static_assert(VALID >= C::STAGES + 5, "ring of masks");
-  __shared__ uint64_t valid_k[VALID], valid_v[C::STAGES];
+  static_assert(VALID >= C::K_STAGES + 5, "ring of masks");
+  __shared__ uint64_t valid_k[VALID], valid_v[C::V_STAGES];
   __shared__ int abort_flag;
   __shared__ int bad_v;                       // some drafted key of this CTA's has a value that is not finite
   __shared__ uint32_t status_word, tmem_slot;
@@ -263,9 +269,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int g = blockIdx.x % a.Hkv, grp = blockIdx.x / a.Hkv;
   grid_launch_next();
   if (tid == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < C::K_STAGES; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 2);
+    }
+    for (int s = 0; s < C::V_STAGES; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], C::E4 ? 1 : 2);
       mbar_init(&v_ready[s], 1);
@@ -314,24 +322,25 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint64_t* full = is_k ? k_full : v_full;
       uint64_t* empty = is_k ? k_empty : v_empty;
       const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V);
+      const int stages = is_k ? C::K_STAGES : C::V_STAGES;
       Producer<C::TILE, C::ELT, D, SMALL> load;
-      int it = 0;
+      int it = 0, st = 0, round = 0;
       bool alive = true;
       for (long long u = u0; u < u1 && alive;) {
         const WidePiece p = wide_piece(pre, len, a, P, u, u1);
         for (int t = p.t0; t < p.t1; ++t, ++it) {
-          const int st = it % C::STAGES, round = it / C::STAGES;
           if (round > 0 && !(alive = wait(&empty[st], (round - 1) & 1))) break;
           load.load(a, is_k ? &a.tm_k : &a.tm_v, p.r, len[p.r], g, t * C::TILE, ring + st * C::KV_BYTES, &full[st],
                     is_k ? &valid_k[it % VALID] : &valid_v[st], &status_word, is_k && it == a.withhold);
+          if (++st == stages) st = 0, ++round;
         }
         u = p.next;
       }
       // Copies in flight end before the CTA does.
       if (*static_cast<volatile int*>(&abort_flag)) {
         volatile int no_abort = 0;
-        for (int i = max(0, it - C::STAGES); i < it; ++i)
-          mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, &status_word, a.wait_limit_ns / 5);
+        for (int i = max(0, it - stages); i < it; ++i)
+          mbar_wait(&full[i % stages], (i / stages) & 1, &no_abort, &status_word, a.wait_limit_ns / 5);
       }
     } else if (warp == 9 || warp == 10) {
       // ---------------------------------------------------------------- MMA issuer of stream s
@@ -353,8 +362,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // S(j), then O += P(j - 1) V
         for (int j = 0; j <= ns && ns > 0; ++j) {
           if (j < ns) {
-            const int it = base + (pair ? j : 2 * j + s), st = it % C::STAGES, c = cs + j, b = c & 1;
-            if (!(alive = wait(&k_full[st], (it / C::STAGES) & 1))) break;
+            const int it = base + (pair ? j : 2 * j + s), st = it % C::K_STAGES, c = cs + j, b = c & 1;
+            if (!(alive = wait(&k_full[st], (it / C::K_STAGES) & 1))) break;
             // P(j - 2), which S(j) overwrites, has been used
             if (j > 1 && !(alive = wait(&pv_done[2 * s + b], ((c >> 1) - 1) & 1))) break;
             tc_fence_after();
@@ -371,9 +380,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (!pair) umma_commit_warp(&k_empty[st]);
           }
           if (j > 0) {
-            const int it = base + (pair ? j - 1 : 2 * (j - 1) + s), st = it % C::STAGES, c = cs + j - 1, b = c & 1;
+            const int it = base + (pair ? j - 1 : 2 * (j - 1) + s), st = it % C::V_STAGES, c = cs + j - 1, b = c & 1;
             const int vs = C::E4 ? it % C::COPIES : st;
-            if (!(alive = wait(&v_ready[vs], (C::E4 ? it / C::COPIES : it / C::STAGES) & 1))) break;
+            if (!(alive = wait(&v_ready[vs], (C::E4 ? it / C::COPIES : it / C::V_STAGES) & 1))) break;
             if (!(alive = wait(&p_full[2 * s + b], (c >> 1) & 1))) break;
             tc_fence_after();
             const uint64_t vd = smem_desc_sw128(
@@ -409,9 +418,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const WidePiece p = wide_piece(pre, len, a, P, u, u1);
         const int keys = len[p.r], base = keys - (P.q_off[p.r + 1] - P.q_off[p.r]);
         for (int t = p.t0; t < p.t1; ++t, ++it) {
-          if ((it & 3) != warp - 12) continue;
-          const int st = it % C::STAGES;
-          if (!(alive = wait(&v_full[st], (it / C::STAGES) & 1))) break;
+          if (it % C::V_WARPS != warp - 12) continue;
+          const int st = it % C::V_STAGES;
+          if (!(alive = wait(&v_full[st], (it / C::V_STAGES) & 1))) break;
           const uint64_t valid = valid_v[st];
           const uint32_t v_at = sbase + C::OFF_V + st * C::KV_BYTES;
           bool bad = false;
