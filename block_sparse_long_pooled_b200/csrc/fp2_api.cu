@@ -50,6 +50,7 @@ int elt_bytes(fp2_dtype t) { return t == FP2_F32 ? 4 : ((t == FP2_BF16 || t == k
 std::atomic<int64_t> g_wait_limit_ns{0};     // 0: the default limit of 1 s
 std::atomic<int64_t> g_withhold_k_tile{-1};  // -1: every load is issued
 std::atomic<int64_t> g_miscount_load{-1};    // -1: every load is counted once (checked builds)
+std::atomic<int64_t> g_late_v_tile{-1};      // -1: loads are issued in order
 
 // Everything derived from (problem, params) on the host.
 struct Ctx {
@@ -533,6 +534,8 @@ uint64_t wait_limit_ns() {
 
 int withheld_k_tile() { return static_cast<int>(g_withhold_k_tile.load()); }
 
+int late_v_tile() { return static_cast<int>(g_late_v_tile.load()); }
+
 fp2_status discover_fixed_scratch(const fp2_problem* problem, const fp2_sparse_params* params,
                                   const fp2_pooled* pooled, const fp2_index* index, void* scratch,
                                   size_t capacity, uint32_t* status_dev, cudaStream_t st) {
@@ -688,6 +691,10 @@ fp2_status fp2_debug_set(int32_t key, int64_t value) {
     case FP2_DEBUG_MISCOUNT_LOAD:
       if (value < -1 || value > 2 * FP2_MAX_BLOCKS) return fail(FP2_ERR_INVALID_ARG, "load must be -1 or in [0, 2 * FP2_MAX_BLOCKS]");
       g_miscount_load.store(value);
+      return FP2_OK;
+    case FP2_DEBUG_LATE_V_TILE:
+      if (value < -1 || value > FP2_MAX_CACHE_LEN) return fail(FP2_ERR_INVALID_ARG, "tile must be -1 or in [0, FP2_MAX_CACHE_LEN]");
+      g_late_v_tile.store(value);
       return FP2_OK;
     default:
       return fail(FP2_ERR_INVALID_ARG, "unknown debug key");

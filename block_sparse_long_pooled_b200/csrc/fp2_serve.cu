@@ -19,6 +19,7 @@ void clear_error();
 void* tensor_map_encoder();
 uint64_t wait_limit_ns();
 int withheld_k_tile();
+int late_v_tile();
 }  // namespace fp2_internal
 
 namespace {
@@ -346,6 +347,7 @@ fp2_status fill_decode(const fp2_decode* p, const DecodeCtx& c, void* scratch, f
   a.scratch = static_cast<uint32_t*>(scratch);
   a.wait_limit_ns = fp2_internal::wait_limit_ns();
   a.withhold = fp2_internal::withheld_k_tile();
+  a.late_v = fp2_internal::late_v_tile();
   return FP2_OK;
 }
 

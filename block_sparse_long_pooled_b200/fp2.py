@@ -36,7 +36,7 @@ EXPORTED = ("fp2_workspace_query", "fp2_workspace_size", "fp2_pool", "fp2_discov
             "fp2_get_device_status", "fp2_last_error", "fp2_version", "fp2_discover_static", "fp2_debug_set",
             "fp2_build_flags", "fp2_rotate", "fp2_decode_workspace", "fp2_tree_attend", "fp2_key_mass",
             "fp2_evict_workspace", "fp2_evict")
-FP2_DEBUG_WAIT_LIMIT_NS, FP2_DEBUG_WITHHOLD_K_TILE, FP2_DEBUG_MISCOUNT_LOAD = 1, 2, 3
+FP2_DEBUG_WAIT_LIMIT_NS, FP2_DEBUG_WITHHOLD_K_TILE, FP2_DEBUG_MISCOUNT_LOAD, FP2_DEBUG_LATE_V_TILE = 1, 2, 3, 4
 FP2_STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -322,8 +322,8 @@ def fp2_get_device_status(scratch) -> tuple:
 
 
 def fp2_debug_set(key: int, value: int):
-    """Testing hook (process-wide): FP2_DEBUG_WAIT_LIMIT_NS, FP2_DEBUG_WITHHOLD_K_TILE or
-    FP2_DEBUG_MISCOUNT_LOAD (checked builds)."""
+    """Testing hook (process-wide): FP2_DEBUG_WAIT_LIMIT_NS, FP2_DEBUG_WITHHOLD_K_TILE,
+    FP2_DEBUG_MISCOUNT_LOAD (checked builds) or FP2_DEBUG_LATE_V_TILE."""
     _check(load_library().fp2_debug_set(int(key), int(value)))
 
 

@@ -296,3 +296,12 @@ def test_reference_eviction():
     assert list(R.evict(w, 10, 4, 1, 1)) == [0, 3, 7, 9]
     assert list(R.evict(w, 10, 5, 0, 0)) == [0, 1, 3, 7, 9]
     assert list(R.evict(w, 10, 3, 2, 1)) == [0, 1, 9]
+
+
+def test_the_late_tile_hook_validates_and_resets():
+    for bad in (-2, fp2.FP2_MAX_CACHE_LEN + 1):
+        with pytest.raises(fp2.FP2Error) as e:
+            fp2.fp2_debug_set(fp2.FP2_DEBUG_LATE_V_TILE, bad)
+        assert e.value.status == INV
+    fp2.fp2_debug_set(fp2.FP2_DEBUG_LATE_V_TILE, 4)
+    fp2.fp2_debug_set(fp2.FP2_DEBUG_LATE_V_TILE, -1)
