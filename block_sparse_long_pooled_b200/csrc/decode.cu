@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
   };
   constexpr int V = D / 32;
   float acc[V], total = 0.f, top = neg_inf();
+  bool some = false;  // a piece so far saw a key of this row
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
   // Up to 32 pieces at a time, lane i with the statistics of piece i; all their rows are on their way
@@ -533,11 +534,12 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
 #pragma unroll
     for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, o));
     now = fmaxf(now, top);
-    // what came before, if anything did (a piece whose scores were all NaN has a sum but no maximum)
-    const float f = total == 0.f ? 0.f : fast_exp2(top - now);
-    total = total == 0.f ? 0.f : total * f;
+    // What came before, if anything did: a piece whose scores were all NaN has a sum but no maximum, and one whose
+    // factor underflows to 0 still hands on an infinity or a NaN of a value (0 x NaN).
+    const float f = some ? fast_exp2(top - now) : 0.f;
+    total = some ? total * f : 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = total == 0.f ? 0.f : acc[e] * f;
+    for (int e = 0; e < V; ++e) acc[e] = some ? acc[e] * f : 0.f;
     top = now;
     // a piece that saw nothing of the row has the sum 0 and may not even have written its part_o
     const bool saw = !(ml.y == 0.f);
@@ -547,6 +549,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     total += sum;
     const uint32_t seen = __ballot_sync(0xFFFFFFFFu, saw);
+    some |= seen != 0;
     for (int i1 = 0; i1 < n; i1 += 16) {
       if (i1 > 0) fetch(i1);
 #pragma unroll

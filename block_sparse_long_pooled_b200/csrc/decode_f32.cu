@@ -33,6 +33,7 @@ struct F32Shared {
   float2 ml[NR];
   long long pre[FP2_MAX_SEQS + 1];
   int len[FP2_MAX_SEQS];
+  uint64_t seen[NR];                // keys of the tile that the row sees, where rows differ in that
   uint32_t valid[2][2];             // keys of the tile that are there
   uint32_t status;
 };
@@ -178,8 +179,11 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const __grid_constan
             const int off = t * kTile + key - base;
             return ((valid >> key) & 1) && m < rows && (off < 0 || (off < 64 && ((word >> off) & 1)));
           };
-          if (!sees(lane)) x0 = neg_inf();
-          if (!sees(lane + 32)) x1 = neg_inf();
+          const bool s0 = sees(lane), s1 = sees(lane + 32);
+          if (!s0) x0 = neg_inf();
+          if (!s1) x1 = neg_inf();
+          const uint32_t low = __ballot_sync(0xFFFFFFFFu, s0), high = __ballot_sync(0xFFFFFFFFu, s1);
+          if (lane == 0) s.seen[rr] = low | (static_cast<uint64_t>(high) << 32);
         }
         float now = fmaxf(x0, x1);
 #pragma unroll
@@ -197,7 +201,8 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const __grid_constan
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < RT; ++i) o[i] *= s.scale[RT * half + i];
-      // A key that a row does not see has the weight 0 there, and its value may be anything (0 x NaN is NaN).
+      // A key that a row does not see has the weight 0 there, and its value may be anything (0 x NaN is NaN): it is
+      // left out.  A key that it does see is not, though its weight may have underflowed to 0.
       const auto add = [&](bool check) {
 #pragma unroll 4
         for (int j = 0; j < kTile; j += 4) {
@@ -208,9 +213,10 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const __grid_constan
           for (int i = 0; i < RT; ++i) {
             const float4 w = *reinterpret_cast<const float4*>(&s.p[RT * half + i][j]);
             const float we[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t in = check ? static_cast<uint32_t>(s.seen[RT * half + i] >> j) : 0u;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (!check || we[e] != 0.f) o[i] = fmaf(we[e], x[e], o[i]);
+              if (!check || ((in >> e) & 1u)) o[i] = fmaf(we[e], x[e], o[i]);
           }
         }
       };

@@ -714,14 +714,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (s == 1 && mine) ml_smem[local] = make_float2(m_run, l_run);
         asm volatile("bar.sync 1, 256;" ::: "memory");
         float top = m_run, total = l_run, f0 = 1.f, f1 = 0.f;
+        bool saw1 = false;  // stream 1 saw a key of the row: its factor may be 0 and its O infinite or NaN
         if (s == 0) {
           const float2 other = mine ? ml_smem[local] : make_float2(neg_inf(), 0.f);
           top = fmaxf(m_run, other.x);
           f0 = l_run == 0.f ? 0.f : fast_exp2(m_run - top);
-          f1 = other.y == 0.f ? 0.f : fast_exp2(other.x - top);
+          saw1 = other.y != 0.f;
+          f1 = saw1 ? fast_exp2(other.x - top) : 0.f;
           total = l_run * f0 + other.y * f1;
           if (l_run == 0.f) total = other.y * f1;
-          if (other.y == 0.f) total = l_run * f0;
+          if (!saw1) total = l_run * f0;
         }
         const float f = total == 0.f ? 0.f : a.v_descale / total;
 #pragma unroll 1
@@ -750,7 +752,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               for (int e = 0; e < 32; ++e) {
                 // a stream that saw nothing of the row leaves zeros
                 float x = l_run == 0.f ? 0.f : __uint_as_float(o[e]) * f0;
-                if (f1 != 0.f) x += buf[(c + e) * 128 + local] * f1;
+                if (saw1) x += buf[(c + e) * 128 + local] * f1;
                 o[e] = __float_as_uint(x);
               }
               if (store) write(o, c0 + c, f);
