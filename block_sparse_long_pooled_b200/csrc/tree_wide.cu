@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
           if (need) {
-            l_run = m_run == neg_inf() ? 0.f : l_run * fast_exp2(m_run - m_new);
+            l_run *= fast_exp2(m_run - m_new);  // (no maximum yet: 0 x 0, or NaN when the scores were NaN)
             m_run = m_new;
           }
           const float off = m_run == neg_inf() ? 0.f : C::P_BIAS - m_run;

@@ -69,3 +69,20 @@ def test_a_seen_value_that_is_not_finite_shows_whatever_its_weight(dtype, d, val
             assert torch.equal(bad, want), (j, int(high.sum()))
             assert torch.isfinite(b.lse).all()
             assert (b.out.float()[~want] - 1).abs().max() <= 2.0 ** -20      # n equal weights of 1: their sum is exact
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("f32", 64)])
+@pytest.mark.parametrize("hq,hkv,n,qlen", [(1, 1, 20001, 1), (4, 1, 20001, 3), (8, 1, 20001, 5), (32, 8, 3000, 5),
+                                           (16, 2, 2000, 40), (4, 4, 300, 3)])
+def test_a_score_that_is_nan_makes_row_and_lse_nan(dtype, d, hq, hkv, n, qlen):
+    """NaN in K, of one key or of whole tiles that every token sees, before and after finite ones."""
+    for j0, j1 in ((0, 1), (0, 64), (0, 200), (77, 78), (n // 2, n // 2 + 100), (n - qlen - 1, n - qlen)):
+        b = Two(dtype, d, hq, hkv, n, qlen, torch.arange(n) % 3 == 0)
+        if dtype == "e4m3":
+            b.k.view(torch.uint8)[0, j0:j1, 0] = 0xFF
+        else:
+            b.k[0, j0:j1, 0] = float("nan")
+        b.attend()
+        g = hq // hkv
+        assert torch.isnan(b.lse[:g]).all() and torch.isfinite(b.lse[g:]).all(), (j0, j1)
+        assert torch.isnan(b.out[:, :g].float()).all() and torch.isfinite(b.out[:, g:].float()).all(), (j0, j1)
