@@ -108,7 +108,7 @@ FP2_DEVICE void store_status(const DecodeArgs& a, const uint32_t* status) {
   __syncthreads();
   if (threadIdx.x == 0) {
     a.scratch[kStatusFirst + blockIdx.x] = *status;
-    if (blockIdx.x == 0) *reinterpret_cast<uint2*>(a.scratch) = make_uint2(0u, kStatusMagic | gridDim.x);
+    if (blockIdx.x == 0) *reinterpret_cast<uint2*>(a.scratch) = make_uint2(kStatusMore, kStatusMagic | gridDim.x);
   }
 }
 

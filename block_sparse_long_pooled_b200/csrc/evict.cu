@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   __syncthreads();
   if (tid == 0) {
     a.scratch[kStatusFirst + blockIdx.x] = s.status;
-    if (blockIdx.x == 0) *reinterpret_cast<uint2*>(a.scratch) = make_uint2(0u, kStatusMagic | gridDim.x);
+    if (blockIdx.x == 0) *reinterpret_cast<uint2*>(a.scratch) = make_uint2(kStatusMore, kStatusMagic | gridDim.x);
   }
 }
 

@@ -652,14 +652,18 @@ fp2_status fp2_prefill(const fp2_problem* problem, const fp2_sparse_params* para
 
 fp2_status fp2_get_device_status(const void* scratch, uint32_t* status_out) {
   if (scratch == nullptr || status_out == nullptr) return fail(FP2_ERR_INVALID_ARG, "NULL argument");
-  uint32_t head[2] = {0, 0};
-  cudaError_t e = cudaMemcpy(head, scratch, sizeof(head), cudaMemcpyDeviceToHost);
+  uint32_t w = 0, more = 0;
+  cudaError_t e = cudaMemcpy(&w, scratch, sizeof(w), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
-  uint32_t w = head[0];
   // Decode and eviction calls leave one word per CTA (serve_kernels.h).
-  if ((head[1] & ~fp2::kStatusCount) == fp2::kStatusMagic) {
+  if (w & fp2::kStatusMore) {
+    w &= ~fp2::kStatusMore;
+    e = cudaMemcpy(&more, static_cast<const uint32_t*>(scratch) + 1, sizeof(more), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(e, "status read");
+  }
+  if ((more & ~fp2::kStatusCount) == fp2::kStatusMagic) {
     uint32_t words[1024];
-    const uint32_t n = head[1] & fp2::kStatusCount;
+    const uint32_t n = more & fp2::kStatusCount;
     for (uint32_t i = 0; i < n; i += 1024) {
       const uint32_t m = std::min<uint32_t>(1024, n - i);
       e = cudaMemcpy(words, static_cast<const uint32_t*>(scratch) + fp2::kStatusFirst + i, m * sizeof(uint32_t),

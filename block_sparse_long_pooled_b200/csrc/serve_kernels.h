@@ -13,9 +13,10 @@ namespace fp2 {
 // Status of the decode and eviction calls.  The prefill clears one word with a memset and its kernels
 // OR into it; at a few microseconds a call, that memset would be a third of a decode step.  Here
 // every CTA keeps its bits in shared memory and stores them to a word of its own when it ends, so
-// nothing has to be cleared: scratch word 0 is zero, word 1 holds kStatusMagic and the number of
+// nothing has to be cleared: scratch word 0 is kStatusMore, word 1 holds kStatusMagic and the number of
 // CTAs, and their words start at byte FP2_SCRATCH_STATUS_BYTES.  fp2_get_device_status reads both
-// forms (the prefill's memset clears word 1).
+// forms, and of a word without kStatusMore no more than that word: it may be a lone one (fp2_rotate's).
+constexpr uint32_t kStatusMore = 0x80000000u;    // no FP2_DEV_* bit
 constexpr uint32_t kStatusMagic = 0x5E000000u;   // low 24 bits: words that follow
 constexpr uint32_t kStatusCount = 0x00FFFFFFu;
 constexpr int kStatusFirst = 256 / 4;            // FP2_SCRATCH_STATUS_BYTES in words

@@ -231,7 +231,8 @@ FP2_API fp2_status fp2_attend(const fp2_problem* problem, const fp2_sparse_param
 FP2_API fp2_status fp2_prefill(const fp2_problem* problem, const fp2_sparse_params* params, void* out, float* lse,
                        void* scratch, size_t scratch_bytes, fp2_stream_t stream);
 
-/* Read the device status word from scratch (a blocking 4-byte copy; call it after
+/* Read the device status word from scratch, or a status_dev word alone (a blocking copy
+ * of its 4 bytes, and of a serving call's scratch of that call's words; call it after
  * the stream has been synchronised).  *status_out gets the raw FP2_DEV_* bits; the
  * return value maps them to FP2_ERR_DEVICE_BOUNDS / FP2_ERR_TIMEOUT, else FP2_OK. */
 FP2_API fp2_status fp2_get_device_status(const void* scratch, uint32_t* status_out);
