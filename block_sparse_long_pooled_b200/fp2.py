@@ -682,7 +682,7 @@ def make_decode(q, cache: Cache, cu_seqlens, kv_len, max_kv_len: int, num_kv_hea
 
 
 def fp2_decode_workspace(decode: Decode) -> int:
-    """Scratch bytes of fp2_tree_attend and fp2_key_mass."""
+    """Scratch bytes of fp2_tree_attend and fp2_key_mass (each its own where both calls' status is read)."""
     n = ctypes.c_size_t(0)
     _check(load_library().fp2_decode_workspace(decode.ref, ctypes.byref(n)))
     return n.value

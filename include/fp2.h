@@ -247,7 +247,9 @@ FP2_API fp2_status fp2_get_device_status(const void* scratch, uint32_t* status_o
  *     [q_len, max_kv_len] sets FP2_DEV_LEN_OOB and the sequence counts as empty;
  *   - scratch belongs to one call at a time: calls that may overlap on the GPU (streams, graphs) take
  *     separate scratch.  The status word of these calls is read the same way, by
- *     fp2_get_device_status on the call's scratch.
+ *     fp2_get_device_status on the call's scratch.  It is the last call's: the next one on the same
+ *     scratch replaces it.  Calls whose status is read after all of them (fp2_tree_attend and the
+ *     fp2_key_mass that follows it) take separate scratch too.
  */
 
 /* A KV cache: K and V are [num_outer, rows, Hkv, d].  With a page table, outer indexes are pages of

@@ -44,3 +44,23 @@ def test_bits_added_to_a_call_s_scratch_are_read_with_its_own():
     b.table_dev[1, 2] = -1
     b.attend()
     assert _status(b.scratch) == (fp2.FP2_ERR_DEVICE_BOUNDS, fp2.FP2_DEV_PAGE_OOB)
+
+
+def test_a_scratch_holds_the_status_of_its_last_call():
+    """The attention meets a page that is out of range, the weights after it do not."""
+    from block_sparse_long_pooled_b200 import fp2
+    b = Batch("bf16", 128, 8, 2, 16, (100, 90), (2, 2), None, seed=4)
+    own = fp2.alloc_scratch(fp2.fp2_decode_workspace(b.handle), "cuda")
+    mass = torch.zeros((2, 2, b.max_len), device="cuda")
+    page = int(b.table[1, 2])
+
+    def step(mass_scratch):
+        b.table_dev[1, 2] = -1
+        b.attend()
+        b.table_dev[1, 2] = page
+        fp2.fp2_key_mass(b.handle, b.lse, None, mass, mass_scratch)
+
+    step(own)
+    assert _status(b.scratch) == (fp2.FP2_ERR_DEVICE_BOUNDS, fp2.FP2_DEV_PAGE_OOB) and _status(own) == (0, 0)
+    step(b.scratch)
+    assert _status(b.scratch) == (0, 0)
