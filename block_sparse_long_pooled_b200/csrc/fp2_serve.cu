@@ -49,6 +49,11 @@ int num_sms() {
   return n;
 }
 
+bool apart(const void* x, size_t x_bytes, const void* y, size_t y_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a + x_bytes <= b || b + y_bytes <= a;
+}
+
 fp2_status check_scratch(const void* scratch, size_t have, size_t need) {
   if (scratch == nullptr) return invalid("scratch is NULL");
   if ((reinterpret_cast<uintptr_t>(scratch) & (kAlign - 1)) != 0) return invalid("scratch must be 256-byte aligned");
@@ -401,10 +406,6 @@ fp2_status fill_evict(const fp2_eviction* p, fp2::EvictArgs& a, int& ranks, size
   if (p->mass_stride < p->max_kv_len) return invalid("mass_stride must be >= max_kv_len");
   // Other CTAs still read the lengths and weights when the first ones write theirs.
   const size_t rows = static_cast<size_t>(p->num_seqs) * p->src.num_kv_heads;
-  const auto apart = [](const void* x, size_t xb, const void* y, size_t yb) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-    return a + xb <= b || b + yb <= a;
-  };
   const size_t mass_bytes = rows * static_cast<size_t>(p->mass_stride) * 4, out_bytes = rows * p->budget * 4;
   const size_t len_bytes = static_cast<size_t>(p->num_seqs) * 4;
   if (!apart(p->kv_len, len_bytes, p->kv_len_out, len_bytes)) return invalid("kv_len_out must not overlap kv_len");
@@ -500,6 +501,15 @@ fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, const float*
   if (!aligned4(lse) || !aligned4(mass_in) || !aligned4(mass_out) || !aligned4(mass_len))
     return invalid("lse, mass_in, mass_out and mass_len must be 4-byte aligned");
   if (mass_out == nullptr || (c.T > 0 && lse == nullptr)) return invalid("lse and mass_out must not be NULL");
+  // A CTA reads old weights, LSE and lengths while others write new weights.
+  const size_t len_bytes = static_cast<size_t>(decode->num_seqs) * 4;
+  const size_t mass_bytes = len_bytes * decode->cache.num_kv_heads * static_cast<size_t>(mass_stride);
+  if (mass_in != nullptr && mass_in != mass_out && !apart(mass_in, mass_bytes, mass_out, mass_bytes))
+    return invalid("mass_in and mass_out must be the same or not overlap");
+  if ((c.T > 0 && !apart(lse, static_cast<size_t>(c.T) * decode->num_q_heads * 4, mass_out, mass_bytes)) ||
+      !apart(decode->kv_len, len_bytes, mass_out, mass_bytes) ||
+      (mass_len != nullptr && !apart(mass_len, len_bytes, mass_out, mass_bytes)))
+    return invalid("mass_out must not overlap lse, kv_len or mass_len");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   fp2::DecodeArgs a;
   fp2::DecodePlan P;

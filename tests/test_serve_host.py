@@ -305,3 +305,24 @@ def test_the_late_tile_hook_validates_and_resets():
         assert e.value.status == INV
     fp2.fp2_debug_set(fp2.FP2_DEBUG_LATE_V_TILE, 4)
     fp2.fp2_debug_set(fp2.FP2_DEBUG_LATE_V_TILE, -1)
+
+
+def test_key_mass_refuses_overlap():
+    """mass_in may be mass_out, not a shifted piece of it; other CTAs still read LSE and lengths."""
+    h = _decode()
+    scratch = fp2.alloc_scratch(fp2.fp2_decode_workspace(h) + 256, "cpu")
+    scratch = scratch[-scratch.data_ptr() % 256:]
+    raw = torch.zeros(1000)
+    mass, lse = torch.zeros((2, 2, 100)), torch.zeros((4, 6))
+    cases = [(dict(lse=lse, mass_in=raw[x:x + 400].view(2, 2, 100), mass_out=raw[100:500].view(2, 2, 100)))
+             for x in (0, 1, 99, 101, 499)]
+    cases.append(dict(lse=raw[:24].view(4, 6), mass_in=None, mass_out=raw[20:420].view(2, 2, 100)))
+    cases.append(dict(lse=lse, mass_in=None, mass_out=mass, mass_len=mass.view(torch.int32).view(-1)[399 - 1:400]))
+    for kw in cases:
+        with pytest.raises(fp2.FP2Error) as e:
+            fp2.fp2_key_mass(h, scratch=scratch, stream=0, **kw)
+        assert e.value.status == INV and "overlap" in str(e.value)
+    h.struct.kv_len = mass.data_ptr()
+    with pytest.raises(fp2.FP2Error) as e:
+        fp2.fp2_key_mass(h, lse, None, mass, scratch, stream=0)
+    assert e.value.status == INV and "overlap" in str(e.value)
