@@ -27,6 +27,8 @@
 // 33 us (14 us of bytes); five of up to 2K to 512 14 us.
 #include <cooperative_groups.h>
 
+#include <cstddef>
+
 #include "fp2_device.cuh"
 #include "serve_kernels.h"
 
@@ -50,7 +52,7 @@ FP2_DEVICE uint32_t ordered(float f) {
 }
 
 struct EvictShared {
-  uint32_t bins[3][kBins];    // this rank's histograms
+  alignas(16) uint32_t bins[3][kBins];  // this rank's histograms, read 16 bytes at a time
   uint32_t groups[3][kGroups];
   uint32_t got[kMaxRanks][kGroups];  // groups, then bins, of every rank
   uint32_t got_bins[kMaxRanks][32];
@@ -58,6 +60,8 @@ struct EvictShared {
   int64_t from[kChunk], to[kChunk];
   uint32_t status;
 };
+static_assert(alignof(EvictShared) >= 16 && kBins * sizeof(uint32_t) % 16 == 0 && kBins == 4 * kThreads, "uint4 of bins");
+static_assert(offsetof(EvictShared, groups) % 8 == 0 && offsetof(EvictShared, got) % 8 == 0, "uint2 of groups");
 
 // Byte offset of (token j, KV head g) of sequence r, or -1 for a page id out of range.
 FP2_DEVICE int64_t row_offset(const CacheView& c, int r, int j, int g, int row_bytes, uint32_t* status) {
