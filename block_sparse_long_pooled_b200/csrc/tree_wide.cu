@@ -20,9 +20,11 @@
 // barriers around its arithmetic.  With few rows the cache's bytes bound the call: 7 tokens by 4 heads at
 // 128K bf16 keys 98 us, 82 of them in the tiles, at 6.5 TB/s.
 //
-// P in bf16 would be off by up to 2^-9 of each weight, as much as the output's own rounding; with at
-// most 128 rows the cache's bytes bound the call, so there a second product adds P - bf16(P), for
-// which S has the columns.  e4m3: P is f16, and V is widened to f16 in shared memory by a warpgroup
+// P in bf16 would be off by up to 2^-8 of each weight, as much as the output's own rounding, so a second
+// product adds P - bf16(P), for which S has the columns: 2^-16.  Up to 128 rows the cache's bytes bound the
+// call and it costs nothing; above that it is 10 to 14 % (eight trees of 33 to 64 tokens by 8 heads on a bf16
+// cache of 9K to 33K keys: 164 us, 150 with one product).  Leaving it out there by the batch's longest draft
+// would make a sequence's precision depend on its neighbours.  e4m3: P is f16, and V is widened to f16 in shared memory by a warpgroup
 // of its own (the products of kind f16 want both operands of one type, and e4m3 weights would keep 4
 // bits).  That warpgroup also clears the rows of V that hold no key, and the elements of a drafted
 // key that are not finite (0 x NaN is NaN for rows that do not see the key); the epilogue adds those
@@ -36,10 +38,10 @@ namespace fp2 {
 
 namespace {
 
-template <int DT, int D, bool SPLIT_>
+template <int DT, int D>
 struct Wide {
   static constexpr bool E4 = DT == 2;
-  static constexpr bool SPLIT = SPLIT_ && !E4;
+  static constexpr bool SPLIT = !E4;
   static constexpr int ELT = E4 ? 1 : 2;
   static constexpr int TILE = kWideTile;
   static constexpr int KCH = 128 / ELT;           // elements of a 128-byte swizzled row
@@ -233,10 +235,10 @@ __device__ __noinline__ void add_cleared(const DecodeArgs& a, int r, int g, int 
   }
 }
 
-template <int DT, int D, bool SPLIT, bool SMALL>
+template <int DT, int D, bool SMALL>
 __global__ void __launch_bounds__(kWideThreads, 1)
     tree_wide_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P) {
-  using C = Wide<DT, D, SPLIT>;
+  using C = Wide<DT, D>;
   extern __shared__ char smem_raw[];
   char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
@@ -787,10 +789,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   store_status(a, &status_word);
 }
 
-template <int DT, int D, bool SPLIT>
+template <int DT, int D>
 cudaError_t run(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
-  using C = Wide<DT, D, SPLIT>;
-  const auto kernel = a.box_rows < 64 ? tree_wide_kernel<DT, D, SPLIT, true> : tree_wide_kernel<DT, D, SPLIT, false>;
+  using C = Wide<DT, D>;
+  const auto kernel = a.box_rows < 64 ? tree_wide_kernel<DT, D, true> : tree_wide_kernel<DT, D, false>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_chained(kernel, dim3(a.groups * a.Hkv), kWideThreads, C::SMEM, stream, 1, a, P);
@@ -799,10 +801,9 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_tree_wide(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
-  const bool split = a.max_rows <= 128;
-  if (dtype == FP2_BF16 && D == 128) return split ? run<1, 128, true>(a, P, stream) : run<1, 128, false>(a, P, stream);
-  if (dtype == FP2_BF16 && D == 64) return split ? run<1, 64, true>(a, P, stream) : run<1, 64, false>(a, P, stream);
-  if (dtype == FP2_E4M3 && D == 128) return run<2, 128, false>(a, P, stream);
+  if (dtype == FP2_BF16 && D == 128) return run<1, 128>(a, P, stream);
+  if (dtype == FP2_BF16 && D == 64) return run<1, 64>(a, P, stream);
+  if (dtype == FP2_E4M3 && D == 128) return run<2, 128>(a, P, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -328,7 +328,9 @@ FP2_API fp2_status fp2_decode_workspace(const fp2_decode* decode, size_t* scratc
  * out: [T, Hq, d] bf16 (f32 over an F32 cache), 16-byte aligned; lse: [Hq, T] f32 natural-log
  * normaliser, or NULL.  A token that sees no key gets zeros and -infinity.  Keys that a token does
  * not see have no influence on it, whatever their values (NaN included); an infinite or NaN value of a
- * key that it does see makes that element infinite or NaN. */
+ * key that it does see makes that element infinite or NaN.  The kernel goes by the batch's longest draft
+ * (up to 16 query rows per KV head, or more), so a long draft can make short ones beside it slower; a
+ * sequence's precision does not depend on the others. */
 FP2_API fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void* scratch,
                                    size_t scratch_bytes, fp2_stream_t stream);
 
