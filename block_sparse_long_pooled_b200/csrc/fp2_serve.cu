@@ -61,6 +61,10 @@ fp2_status check_scratch(const void* scratch, size_t have, size_t need) {
   return FP2_OK;
 }
 
+fp2_status check_stream(fp2_stream_t stream) {
+  return stream == FP2_STREAM_NONE ? invalid("the buffers are not on a GPU") : FP2_OK;
+}
+
 fp2_status clear_status(void* scratch, cudaStream_t st) {
   return launched(cudaMemsetAsync(scratch, 0, FP2_SCRATCH_STATUS_BYTES, st));
 }
@@ -443,6 +447,7 @@ fp2_status fp2_rotate(const fp2_rotation* rotation, uint32_t* status_dev, fp2_st
   FP2_TRY(check_rotation(rotation));
   if (!aligned4(status_dev)) return invalid("status_dev must be 4-byte aligned");
   if (rotation->tokens == 0) return FP2_OK;
+  FP2_TRY(check_stream(stream));
   return run_rotate(rotation, status_dev, static_cast<cudaStream_t>(stream));
 }
 
@@ -462,6 +467,7 @@ fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void
   FP2_TRY(check_scratch(scratch, scratch_bytes, c.bytes));
   if ((c.T > 0 && out == nullptr) || !aligned16(out)) return invalid("out must be a 16-byte aligned pointer");
   if (!aligned4(lse)) return invalid("lse must be 4-byte aligned");
+  FP2_TRY(check_stream(stream));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (c.T == 0) return clear_status(scratch, st);
   fp2::DecodeArgs a;
@@ -510,6 +516,7 @@ fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, const float*
       !apart(decode->kv_len, len_bytes, mass_out, mass_bytes) ||
       (mass_len != nullptr && !apart(mass_len, len_bytes, mass_out, mass_bytes)))
     return invalid("mass_out must not overlap lse, kv_len or mass_len");
+  FP2_TRY(check_stream(stream));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   fp2::DecodeArgs a;
   fp2::DecodePlan P;
@@ -545,6 +552,7 @@ fp2_status fp2_evict(const fp2_eviction* eviction, void* scratch, size_t scratch
   size_t need = 0;
   FP2_TRY(fill_evict(eviction, a, ranks, need));
   FP2_TRY(check_scratch(scratch, scratch_bytes, need));
+  FP2_TRY(check_stream(stream));
   a.scratch = static_cast<uint32_t*>(scratch);
   return launched(fp2::launch_evict(a, ranks, static_cast<cudaStream_t>(stream)));
 }

@@ -38,6 +38,7 @@ EXPORTED = ("fp2_workspace_query", "fp2_workspace_size", "fp2_pool", "fp2_discov
             "fp2_evict_workspace", "fp2_evict")
 FP2_DEBUG_WAIT_LIMIT_NS, FP2_DEBUG_WITHHOLD_K_TILE, FP2_DEBUG_MISCOUNT_LOAD, FP2_DEBUG_LATE_V_TILE = 1, 2, 3, 4
 FP2_STATIC_SCRATCH_BYTES = 8 << 20
+FP2_STREAM_NONE = ctypes.c_void_p(-1).value
 
 
 class fp2_problem(ctypes.Structure):
@@ -460,9 +461,10 @@ class _Handle:
             self.guard, self.alone = torch.cuda.device, torch.cuda.device_count() == 1
 
     def call(self, fn, args, stream):
-        """The C entry point fn on this handle, on its device and (stream None) that device's current stream."""
-        if not self.cuda:
-            status = fn(self.ref, *args, 0 if stream is None else _stream_handle(stream))
+        """The C entry point fn on this handle, on its device and (stream None) that device's current stream.
+        Tensors of the host are refused."""
+        if not self.cuda:       # host memory: the library's checks, and then its refusal
+            status = fn(self.ref, *args, FP2_STREAM_NONE)
         else:
             raw = self.raw_stream(self.index) if stream is None else _stream_handle(stream)
             if self.alone or self.current() == self.index:

@@ -249,8 +249,11 @@ FP2_API fp2_status fp2_get_device_status(const void* scratch, uint32_t* status_o
  *     separate scratch.  The status word of these calls is read the same way, by
  *     fp2_get_device_status on the call's scratch.  It is the last call's: the next one on the same
  *     scratch replaces it.  Calls whose status is read after all of them (fp2_tree_attend and the
- *     fp2_key_mass that follows it) take separate scratch too.
+ *     fp2_key_mass that follows it) take separate scratch too;
+ *   - given FP2_STREAM_NONE as their stream these calls check their arguments and refuse the rest:
+ *     for a binding whose buffers turn out to be in host memory.
  */
+#define FP2_STREAM_NONE ((fp2_stream_t)-1)
 
 /* A KV cache: K and V are [num_outer, rows, Hkv, d].  With a page table, outer indexes are pages of
  * `rows` tokens and token j of sequence r is row j % rows of page page_table[r][j / rows]; without

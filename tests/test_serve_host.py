@@ -326,3 +326,22 @@ def test_key_mass_refuses_overlap():
     with pytest.raises(fp2.FP2Error) as e:
         fp2.fp2_key_mass(h, lse, None, mass, scratch, stream=0)
     assert e.value.status == INV and "overlap" in str(e.value)
+
+
+def test_tensors_of_the_host_are_refused():
+    """Every other check passes: a kernel that got these pointers would fault the GPU."""
+    h, e = _decode(), _evict(paged_out=True)
+    scratch = fp2.alloc_scratch(max(fp2.fp2_decode_workspace(h), fp2.fp2_evict_workspace(e)) + 256, "cpu")
+    scratch = scratch[-scratch.data_ptr() % 256:]
+    none = fp2.make_decode(torch.zeros((0, 4, 128), dtype=torch.bfloat16),
+                           fp2.make_cache(*(torch.zeros((1, 50, 2, 128), dtype=torch.bfloat16) for _ in "kv")), [0, 0],
+                           torch.zeros(1, dtype=torch.int32), 50)
+    out, lse, mass = torch.zeros((6, 4, 128), dtype=torch.bfloat16), torch.zeros((4, 6)), torch.zeros((2, 2, 100))
+    for call in (lambda s: fp2.fp2_rotate(_rotation(), stream=s), lambda s: fp2.fp2_evict(e, scratch, stream=s),
+                 lambda s: fp2.fp2_tree_attend(h, out, lse, scratch, stream=s),
+                 lambda s: fp2.fp2_tree_attend(none, out[:0], lse[:, :0].contiguous(), scratch, stream=s),
+                 lambda s: fp2.fp2_key_mass(h, lse, None, mass, scratch, stream=s)):
+        for stream in (None, 0):
+            with pytest.raises(fp2.FP2Error) as err:
+                call(stream)
+            assert err.value.status == INV and "GPU" in str(err.value)
