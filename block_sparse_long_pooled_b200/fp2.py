@@ -609,9 +609,9 @@ def make_rotate(q, k, v, positions, rope: Optional[Rope], q_out, k_out, v_out, s
         s.num_q_heads, s.q, s.q_stride_tok = q.shape[1], _ptr(q), stride(q)
         s.q_out, s.q_out_stride_tok = _ptr(q_out), stride(q_out)
     if k is not None:
-        rows, steps = None, []
+        rows, steps = [], []
         for x, o, n in outs:
-            if x is q:
+            if n == "q_out":        # (by name: q may be the tensor that k is)
                 continue
             _head_rows(o, n, o.dim())
             if o.dim() not in (3, 4) or tuple(o.shape[-2:]) != tuple(x.shape[1:]):
@@ -620,8 +620,8 @@ def make_rotate(q, k, v, positions, rope: Optional[Rope], q_out, k_out, v_out, s
             if o.dim() == 4 and o.shape[0] > 1 and o.stride(0) != o.shape[1] * step:
                 raise ValueError(f"pages of {n} must follow each other without a gap")
             steps.append(step)
-            rows = o.shape[0] if o.dim() == 3 else o.shape[0] * o.shape[1]
-            s.num_slots = rows if not s.num_slots else min(rows, s.num_slots)
+            rows.append(o.shape[0] if o.dim() == 3 else o.shape[0] * o.shape[1])
+        s.num_slots = min(rows)
         if len(set(steps)) != 1:
             raise ValueError("k_out and v_out must have the same token stride")
         s.num_kv_heads, s.k, s.k_stride_tok, s.k_out = k.shape[1], _ptr(k), stride(k), _ptr(k_out)

@@ -345,3 +345,18 @@ def test_tensors_of_the_host_are_refused():
             with pytest.raises(fp2.FP2Error) as err:
                 call(stream)
             assert err.value.status == INV and "GPU" in str(err.value)
+
+
+def test_make_rotate_of_one_tensor_as_q_and_k():
+    """K's output is checked although Q is the same tensor, and the rows are the smaller cache's, be it empty."""
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    x, rope, pos = z(4, 2, 64), fp2.make_rope(fp2.rope_frequencies(64)[0]), torch.zeros(4, dtype=torch.int32)
+    h = fp2.make_rotate(x, x, x, pos, rope, z(4, 2, 64), z(9, 2, 64), z(7, 2, 64))
+    assert h.struct.num_slots == 7 and h.struct.kv_out_stride_tok == 128
+    h = fp2.make_rotate(x, x, z(4, 2, 64), pos, rope, z(4, 2, 64), z(5, 2, 64), z(7, 2, 64))
+    assert h.struct.num_slots == 5
+    for bad in (z(4, 3, 64), z(4, 2, 32), z(4, 4, 64)[:, ::2]):
+        with pytest.raises(ValueError):
+            fp2.make_rotate(x, x, z(4, 2, 64), pos, rope, z(4, 2, 64), bad, z(7, 2, 64))
+    h = fp2.make_rotate(None, x, x, pos, rope, None, z(0, 2, 64), z(7, 2, 64), slots=torch.zeros(4, dtype=torch.int64))
+    assert h.struct.num_slots == 0
