@@ -619,8 +619,10 @@ def make_rotate(q, k, v, positions, rope: Optional[Rope], q_out, k_out, v_out, s
             step = o.stride(-3) if o.shape[-3] > 1 else (o.stride(0) if o.dim() == 4 else o.shape[-2] * o.shape[-1])
             if o.dim() == 4 and o.shape[0] > 1 and o.stride(0) != o.shape[1] * step:
                 raise ValueError(f"pages of {n} must follow each other without a gap")
-            steps.append(step)
             rows.append(o.shape[0] if o.dim() == 3 else o.shape[0] * o.shape[1])
+            if rows[-1] > 1 and step < o.shape[-2] * o.shape[-1]:
+                raise ValueError(f"rows of {n} overlap")
+            steps.append(step)
         s.num_slots = min(rows)
         if len(set(steps)) != 1:
             raise ValueError("k_out and v_out must have the same token stride")

@@ -360,3 +360,12 @@ def test_make_rotate_of_one_tensor_as_q_and_k():
             fp2.make_rotate(x, x, z(4, 2, 64), pos, rope, z(4, 2, 64), bad, z(7, 2, 64))
     h = fp2.make_rotate(None, x, x, pos, rope, None, z(0, 2, 64), z(7, 2, 64), slots=torch.zeros(4, dtype=torch.int64))
     assert h.struct.num_slots == 0
+
+
+def test_make_rotate_refuses_rows_that_overlap():
+    """An expanded output has room for one row, whatever its shape says."""
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    for out in (z(1, 2, 64).expand(4, 2, 64), z(1, 16, 2, 64)[:, :1].expand(1, 16, 2, 64), z(1, 1, 2, 64).expand(4, 1, 2, 64)):
+        with pytest.raises(ValueError):
+            fp2.make_rotate(None, z(4, 2, 64), None, None, None, None, out, None)
+    assert fp2.make_rotate(None, z(1, 2, 64), None, None, None, None, z(1, 2, 64).expand(1, 2, 64), None).struct.num_slots == 1
