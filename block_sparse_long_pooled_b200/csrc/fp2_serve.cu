@@ -283,12 +283,22 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// Encodes a map.  The encoder is a driver call, which wants a current context; a thread that has made no runtime call
+// yet has none (these calls' maps come before their first launch), and gets its device's then.
+template <typename Encode>
+fp2_status encode(const Encode& map) {
+  const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(fp2_internal::tensor_map_encoder());
+  if (fn == nullptr) return fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  CUresult r = map(fn);
+  int dev = 0;
+  if (r != CUDA_SUCCESS && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = map(fn);
+  return r == CUDA_SUCCESS ? FP2_OK : fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+}
+
 int box_rows(const fp2_cache& c) { return c.page_table != nullptr ? std::min(c.rows, 64) : 64; }
 
 // [outer][token][head][d] with boxes of 128 bytes x up to 64 tokens; a box never leaves its page.
 fp2_status encode_cache(CUtensorMap* m, const fp2_cache& c, void* base) {
-  const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(fp2_internal::tensor_map_encoder());
-  if (fn == nullptr) return fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const int elt = elt_bytes(c.dtype);
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.num_kv_heads),
                               static_cast<cuuint64_t>(c.rows), static_cast<cuuint64_t>(c.num_outer)};
@@ -298,16 +308,15 @@ fp2_status encode_cache(CUtensorMap* m, const fp2_cache& c, void* base) {
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / elt), 1u,
                              static_cast<cuuint32_t>(box_rows(c)), 1u};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  const CUresult r = fn(m, c.dtype == FP2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
-                        base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FP2_OK : fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  return encode([&](EncodeTiledFn fn) {
+    return fn(m, c.dtype == FP2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 // [token][head][d] with boxes of 128 bytes x the heads of a group x `tokens`.
 fp2_status encode_q(CUtensorMap* m, const fp2_decode* p, int T, int G, int tokens) {
-  const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(fp2_internal::tensor_map_encoder());
-  if (fn == nullptr) return fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const fp2_cache& c = p->cache;
   const int elt = elt_bytes(c.dtype);
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(p->num_q_heads),
@@ -317,11 +326,11 @@ fp2_status encode_q(CUtensorMap* m, const fp2_decode* p, int T, int G, int token
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(G),
                              static_cast<cuuint32_t>(tokens)};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
-  const CUresult r = fn(m, c.dtype == FP2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-                        const_cast<void*>(p->q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FP2_OK : fail(FP2_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  return encode([&](EncodeTiledFn fn) {
+    return fn(m, c.dtype == FP2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+              const_cast<void*>(p->q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 fp2_status fill_decode(const fp2_decode* p, const DecodeCtx& c, void* scratch, fp2::DecodeArgs& a,
