@@ -148,6 +148,16 @@ fp2_status check_rotation(const fp2_rotation* p) {
     if (p->slots != nullptr ? !aligned8(p->slots) || p->num_slots < 0 : p->num_slots < p->tokens)
       return invalid("num_slots must cover every token (or slots be given, 8-byte aligned)");
   }
+  // In place every value is read and written by one thread, if it goes to where it came from.
+  const auto in_place_ok = [&](const void* x, int64_t stride, const void* out, int64_t out_stride, bool moved) {
+    return x != out || (p->out_dtype == p->in_dtype && !moved && (stride == out_stride || p->tokens == 1));
+  };
+  const bool moved = p->slots != nullptr;
+  if ((p->num_q_heads > 0 && !in_place_ok(p->q, p->q_stride_tok, p->q_out, p->q_out_stride_tok, false)) ||
+      (p->num_kv_heads > 0 && !in_place_ok(p->k, p->k_stride_tok, p->k_out, p->kv_out_stride_tok, moved)) ||
+      (p->num_kv_heads > 0 && p->v != nullptr &&
+       !in_place_ok(p->v, p->v_stride_tok, p->v_out, p->kv_out_stride_tok, moved)))
+    return invalid("an output in place needs its input's type and stride, and for K and V no slots");
   if (!aligned16(p->q_norm) || !aligned16(p->k_norm)) return invalid("norm weights must be 16-byte aligned");
   return FP2_OK;
 }

@@ -301,7 +301,7 @@ typedef struct {
 /* Rotate: x' = norm(x) per head, pairs of the first rotary_dim values turn by their angle, V passes
  * through; one rounding, to out_dtype (E4M3 saturates at 448).  Angles are exact at any int32
  * position (no fp32 product of position and frequency).  An output may be its own input (same
- * pointer, stride and type; without slots); otherwise outputs must not overlap inputs.  Slots that
+ * pointer, stride and type; K and V without slots); otherwise outputs must not overlap inputs.  Slots that
  * are >= 0 must be distinct.  status_dev: device word that FP2_DEV_* bits are OR-ed into, or NULL;
  * not cleared.  No scratch. */
 FP2_API fp2_status fp2_rotate(const fp2_rotation* rotation, uint32_t* status_dev, fp2_stream_t stream);

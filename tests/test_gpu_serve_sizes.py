@@ -125,3 +125,29 @@ def test_pages_that_hold_k_and_v_side_by_side(dtype, d, qlen):
     b.cache = fp2.make_cache(both[:, 0], both[:, 1], b.table_dev)
     b.handle = fp2.make_decode(b.q, b.cache, b.cu, b.kv_len, b.max_len, b.hkv, tree_mask=b.words_dev, **b.descale)
     _attend_and_weigh(b)
+
+
+@pytest.mark.parametrize("tokens,hq,hkv,inter", [(5, 8, 2, False), (300, 32, 8, True), (5000, 3, 1, False), (20000, 8, 2, True)])
+def test_rotate_in_place_inside_one_projection(tokens, hq, hkv, inter):
+    """Q in its own place, a view of the projection's output, while K and V go to the slots of a cache; then all three
+    in place.  The same bits as into buffers of their own, and nothing else of the projection changes."""
+    from block_sparse_long_pooled_b200 import fp2
+    g, d = _gen(12), 128
+    x = torch.randn((tokens, hq + 2 * hkv + 1, d), generator=g).to(torch.bfloat16).cuda()
+    cut = lambda t: (t[:, :hq], t[:, hq:hq + hkv], t[:, hq + hkv:hq + 2 * hkv])  # noqa: E731
+    w = (1 + 0.3 * torch.randn(d, generator=g)).to(torch.bfloat16).cuda()
+    pos = torch.randint(0, 1 << 17, (tokens,), generator=g).to(torch.int32).cuda()
+    rope = fp2.make_rope(fp2.rope_frequencies(64)[0], inter)
+    slots = torch.randperm(tokens + 7, generator=g)[:tokens].cuda()
+    rows = lambda: torch.zeros((tokens + 7, hkv, d), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    own = [torch.zeros((tokens, hq, d), dtype=torch.bfloat16, device="cuda"), rows(), rows()]
+    fp2.fp2_rotate(fp2.make_rotate(*cut(x), pos, rope, *own, slots=slots, q_norm=w, k_norm=w))
+    y, k, v = x.clone(), rows(), rows()
+    fp2.fp2_rotate(fp2.make_rotate(*cut(y), pos, rope, cut(y)[0], k, v, slots=slots, q_norm=w, k_norm=w))
+    assert torch.equal(cut(y)[0], own[0]) and torch.equal(k, own[1]) and torch.equal(v, own[2])
+    assert torch.equal(y[:, hq:], x[:, hq:])
+    y = x.clone()
+    fp2.fp2_rotate(fp2.make_rotate(*cut(y), pos, rope, *cut(y), q_norm=w, k_norm=w))
+    for got, want in zip(cut(y), (own[0], own[1][slots], own[2][slots])):
+        assert torch.equal(got, want)
+    assert torch.equal(y[:, -1], x[:, -1])

@@ -369,3 +369,25 @@ def test_make_rotate_refuses_rows_that_overlap():
         with pytest.raises(ValueError):
             fp2.make_rotate(None, z(4, 2, 64), None, None, None, None, out, None)
     assert fp2.make_rotate(None, z(1, 2, 64), None, None, None, None, z(1, 2, 64).expand(1, 2, 64), None).struct.num_slots == 1
+
+
+def test_rotate_in_place_needs_the_input_s_type_and_stride():
+    z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)  # noqa: E731
+    pos, rope = z(4, t=torch.int32), fp2.make_rope(fp2.rope_frequencies(64)[0])
+    q, k, v, slots = z(4, 4, 64), z(4, 2, 64), z(4, 2, 64), z(4, t=torch.int64)
+    wide = z(4, 8, 64)
+    good = dict(q=q, k=k, v=v, positions=pos, rope=rope, q_out=q, k_out=k, v_out=v)
+    with pytest.raises(fp2.FP2Error) as e:       # all is well up to the buffers' being on the host
+        fp2.fp2_rotate(fp2.make_rotate(**good))
+    assert "GPU" in str(e.value)
+    for bad in (dict(slots=slots), dict(slots=slots, v_out=z(4, 2, 64)), dict(q_out=wide.view(-1)[:4 * 256].view(4, 4, 64), q=wide[:, :4]),
+                dict(k=wide[:, :2], k_out=wide.view(-1)[:4 * 128].view(4, 2, 64)),
+                dict(v=wide[:, :2], v_out=wide.view(-1)[:4 * 128].view(4, 2, 64))):
+        with pytest.raises(fp2.FP2Error) as e:
+            fp2.fp2_rotate(fp2.make_rotate(**{**good, **bad}))
+        assert e.value.status == INV and "in place" in str(e.value)
+    one = _rotation(q=None)
+    one.struct.q, one.struct.out_dtype = one.struct.q_out, fp2.FP2_E4M3
+    with pytest.raises(fp2.FP2Error) as e:
+        fp2.fp2_rotate(one)
+    assert e.value.status == INV and "in place" in str(e.value)
