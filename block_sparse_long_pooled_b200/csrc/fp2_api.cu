@@ -50,7 +50,7 @@ int elt_bytes(fp2_dtype t) { return t == FP2_F32 ? 4 : ((t == FP2_BF16 || t == k
 std::atomic<int64_t> g_wait_limit_ns{0};     // 0: the default limit of 1 s
 std::atomic<int64_t> g_withhold_k_tile{-1};  // -1: every load is issued
 std::atomic<int64_t> g_miscount_load{-1};    // -1: every load is counted once (checked builds)
-std::atomic<int64_t> g_late_v_tile{-1};      // -1: loads are issued in order
+std::atomic<int64_t> g_late_v_tile{-1};      // -1: loads are issued in order (checked builds)
 
 // Everything derived from (problem, params) on the host.
 struct Ctx {

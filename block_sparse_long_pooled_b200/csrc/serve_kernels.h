@@ -121,7 +121,7 @@ struct DecodeArgs {
   uint32_t* scratch;          // status words: see StatusWords
   uint64_t wait_limit_ns;
   int withhold;               // testing: the producer skips the load of this local key tile (-1: none)
-  int late_v;                 // testing, tree_wide.cu: this V tile is loaded after the two that follow it (-1: none)
+  int late_v;                 // testing, checked builds, tree_wide.cu: this V tile is loaded after the two behind it (-1: none)
 };
 
 // Tree attention kernels: up to kFewRows query rows per (sequence, KV head) decode.cu, above that

@@ -326,25 +326,28 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V);
       const int stages = is_k ? C::K_STAGES : C::V_STAGES;
       Producer<C::TILE, C::ELT, D, SMALL> load;
-      int it = 0, st = 0, round = 0, late_t = -1, late_st = 0;
+      int it = 0, st = 0, round = 0;
+      [[maybe_unused]] int late_t = -1, late_st = 0;
       bool alive = true;
       for (long long u = u0; u < u1 && alive;) {
         const WidePiece p = wide_piece(pre, len, a, P, u, u1);
         for (int t = p.t0; t < p.t1; ++t, ++it) {
           if (round > 0 && !(alive = wait(&empty[st], (round - 1) & 1))) break;
-          int what = t, where = st, turns = 1;
-          if (!is_k && a.late_v >= 0) {  // testing: this load follows the next two of the piece
-            if (it == a.late_v && t + 2 < p.t1) late_t = t, late_st = st, turns = 0;
-            if (late_t >= 0 && it == a.late_v + 2) turns = 2;
-          }
-#pragma unroll 1
-          while (turns-- > 0) {
-            load.load(a, is_k ? &a.tm_k : &a.tm_v, p.r, len[p.r], g, what * C::TILE, ring + where * C::KV_BYTES,
-                      &full[where], is_k ? &valid_k[it % VALID] : &valid_v[where], &status_word, is_k && it == a.withhold);
-            if (turns > 0) {
+          const auto bring = [&](int t, int st) {
+            load.load(a, is_k ? &a.tm_k : &a.tm_v, p.r, len[p.r], g, t * C::TILE, ring + st * C::KV_BYTES, &full[st],
+                      is_k ? &valid_k[it % VALID] : &valid_v[st], &status_word, is_k && it == a.withhold);
+          };
+          if constexpr (FP2_CHECKED) {   // testing: one V tile follows the next two of its piece
+            const bool held = !is_k && it == a.late_v && t + 2 < p.t1;
+            if (held) late_t = t, late_st = st;
+            else bring(t, st);
+            if (late_t >= 0 && it == a.late_v + 2) {
               __nanosleep(50000);
-              what = late_t, where = late_st, late_t = -1;
+              bring(late_t, late_st);
+              late_t = -1;
             }
+          } else {
+            bring(t, st);
           }
           if (++st == stages) st = 0, ++round;
         }

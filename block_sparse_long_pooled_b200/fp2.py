@@ -323,8 +323,8 @@ def fp2_get_device_status(scratch) -> tuple:
 
 
 def fp2_debug_set(key: int, value: int):
-    """Testing hook (process-wide): FP2_DEBUG_WAIT_LIMIT_NS, FP2_DEBUG_WITHHOLD_K_TILE,
-    FP2_DEBUG_MISCOUNT_LOAD (checked builds) or FP2_DEBUG_LATE_V_TILE."""
+    """Testing hook (process-wide): FP2_DEBUG_WAIT_LIMIT_NS, FP2_DEBUG_WITHHOLD_K_TILE, and in
+    checked builds FP2_DEBUG_MISCOUNT_LOAD or FP2_DEBUG_LATE_V_TILE."""
     _check(load_library().fp2_debug_set(int(key), int(value)))
 
 

@@ -404,9 +404,10 @@ FP2_API fp2_status fp2_discover_static(const fp2_problem* problem, const fp2_spa
  *                              hand-off counters, so the consumer's check of that load fails and
  *                              the status word gets FP2_DEV_CHECK.  The data path is unchanged;
  *                              the normal build ignores it.
- *   FP2_DEBUG_LATE_V_TILE      fp2_tree_attend with more than 16 query rows per KV head, caches other than F32: the
- *                              producer of every CTA loads its local V tile `value` (-1 restores normal
- *                              operation) some 50 us after the two tiles that follow it.  Results do not change.
+ *   FP2_DEBUG_LATE_V_TILE      checked builds only, fp2_tree_attend with more than 16 query rows per KV head and
+ *                              caches other than F32: the producer of every CTA loads its local V tile `value`
+ *                              (-1 restores normal operation) some 50 us after the two tiles that follow it.
+ *                              Results do not change; the normal build ignores it.
  * The first two also hold for fp2_tree_attend and fp2_key_mass (F32 caches apart, whose kernels wait for
  * no barrier): the limit of their waits, and every producer skips the K load of its local key tile `value`.
  * Returns FP2_ERR_INVALID_ARG for an unknown key or a value out of range. */
