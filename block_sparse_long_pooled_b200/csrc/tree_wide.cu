@@ -20,11 +20,12 @@
 // barriers around its arithmetic.  With few rows the cache's bytes bound the call: 7 tokens by 4 heads at
 // 128K bf16 keys 98 us, 82 of them in the tiles, at 6.5 TB/s.
 //
-// P in bf16 would be off by up to 2^-8 of each weight, as much as the output's own rounding, so a second
-// product adds P - bf16(P), for which S has the columns: 2^-16.  Up to 128 rows the cache's bytes bound the
-// call and it costs nothing; above that it is 10 to 14 % (eight trees of 33 to 64 tokens by 8 heads on a bf16
-// cache of 9K to 33K keys: 164 us, 150 with one product).  Leaving it out there by the batch's longest draft
-// would make a sequence's precision depend on its neighbours.  e4m3: P is f16, and V is widened to f16 in shared memory by a warpgroup
+// P in bf16 is off by up to 2^-8 of each weight, as much as the output's own rounding.  For sequences of up to
+// 128 rows, where the cache's bytes bound the call, a second product adds P - bf16(P) (2^-16), for which S has
+// the columns: 7 tokens by 4 heads at 128K bf16 keys take 96 us with it, 91 without.  Above 128 rows, where
+// products and softmax do, P stays single: eight trees of 33 to 64 tokens by 8 heads on a bf16 cache of 9K to
+// 33K keys take 147 us, 161 with both.  The choice goes by the sequence's own rows: by the batch's longest
+// draft, a sequence's precision would depend on its neighbours.  e4m3: P is f16, and V is widened to f16 in shared memory by a warpgroup
 // of its own (the products of kind f16 want both operands of one type, and e4m3 weights would keep 4
 // bits).  That warpgroup also clears the rows of V that hold no key, and the elements of a drafted
 // key that are not finite (0 x NaN is NaN for rows that do not see the key); the epilogue adds those
@@ -41,7 +42,6 @@ namespace {
 template <int DT, int D>
 struct Wide {
   static constexpr bool E4 = DT == 2;
-  static constexpr bool SPLIT = !E4;
   static constexpr int ELT = E4 ? 1 : 2;
   static constexpr int TILE = kWideTile;
   static constexpr int KCH = 128 / ELT;           // elements of a 128-byte swizzled row
@@ -85,6 +85,9 @@ struct Wide {
   static_assert(MERGE % 32 == 0 && D % MERGE == 0, "merge rounds");
 };
 constexpr int kWideThreads = 512;
+
+// bf16: whether the weights of a sequence of so many rows go to the tensor cores as hi + lo.
+__host__ FP2_DEVICE bool split_weights(int rows) { return rows > 0 && rows <= 128; }
 
 // Weighted pieces: an item (sequence, pair of M tiles) spans w * tiles units, w = its M tiles.
 struct WidePiece {
@@ -235,7 +238,8 @@ __device__ __noinline__ void add_cleared(const DecodeArgs& a, int r, int g, int 
   }
 }
 
-template <int DT, int D, bool SMALL>
+// SPLIT: the batch has sequences whose weights come as hi + lo (split_weights).
+template <int DT, int D, bool SPLIT, bool SMALL>
 __global__ void __launch_bounds__(kWideThreads, 1)
     tree_wide_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodePlan P) {
   using C = Wide<DT, D>;
@@ -371,6 +375,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const bool pair = p.w == 2;
         u = p.next;
         const int ns = pair ? n : (n + 1 - s) / 2;  // tiles of this stream
+        const int parts = SPLIT && split_weights((P.q_off[p.r + 1] - P.q_off[p.r]) * a.G) ? 2 : 1;
         if (ns > 0) {
           if (!(alive = wait(&q_ready[s], nq++ & 1))) break;
           tc_fence_after();
@@ -405,7 +410,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const uint64_t vd = smem_desc_sw128(
                 sbase + (C::E4 ? C::OFF_V16 + vs * C::V16_BYTES : C::OFF_V + st * C::KV_BYTES), C::TILE * 128, 1024);
 #pragma unroll
-            for (int part = 0; part < (C::SPLIT ? 2 : 1); ++part) {
+            for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+              if (part >= parts) break;
 #pragma unroll
               for (int k = 0; k < C::TILE / 16; ++k)
                 umma_ts_warp<1>(o_col, s_col + b * 64 + part * 32 + k * 8,
@@ -548,6 +554,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const bool mine = local >= 0 && row < rows;
       const int tok = mine ? row / a.G : 0, h = g * a.G + (mine ? row - tok * a.G : 0);
       const bool busy = __any_sync(0xFFFFFFFFu, mine);
+      [[maybe_unused]] const bool split = SPLIT && split_weights(rows);
       const int n = p.t1 - p.t0;
 
       // Q: the warp's 32 rows, RPL of them at a time with their chunks side by side in the lanes, every load
@@ -642,19 +649,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t hi[16];
-            [[maybe_unused]] uint32_t lo[16];
+            float2 w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 x = __ffma2_rn(
                   make_float2(__uint_as_float(v[32 * c + 2 * e]), __uint_as_float(v[32 * c + 2 * e + 1])), s22, off2);
-              const float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              acc[e & 1] = __fadd2_rn(acc[e & 1], w);
-              hi[e] = C::E4 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
-              if constexpr (C::SPLIT)
-                lo[e] = pack_bf16x2(w.x - __uint_as_float(hi[e] << 16), w.y - __uint_as_float(hi[e] & 0xFFFF0000u));
+              w[e] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              acc[e & 1] = __fadd2_rn(acc[e & 1], w[e]);
+              hi[e] = C::E4 ? pack_f16x2(w[e].x, w[e].y) : pack_bf16x2(w[e].x, w[e].y);
             }
             tmem_st16(s_at + 64 * b + 16 * c, hi);
-            if constexpr (C::SPLIT) tmem_st16(s_at + 64 * b + 32 + 16 * c, lo);
+            if (SPLIT && split) {
+              uint32_t lo[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                lo[e] = pack_bf16x2(w[e].x - __uint_as_float(hi[e] << 16), w[e].y - __uint_as_float(hi[e] & 0xFFFF0000u));
+              tmem_st16(s_at + 64 * b + 32 + 16 * c, lo);
+            }
           }
           l_run += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
           tmem_st_wait();
@@ -792,10 +803,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   store_status(a, &status_word);
 }
 
-template <int DT, int D>
+template <int DT, int D, bool SPLIT>
 cudaError_t run(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
   using C = Wide<DT, D>;
-  const auto kernel = a.box_rows < 64 ? tree_wide_kernel<DT, D, true> : tree_wide_kernel<DT, D, false>;
+  const auto kernel = a.box_rows < 64 ? tree_wide_kernel<DT, D, SPLIT, true> : tree_wide_kernel<DT, D, SPLIT, false>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_chained(kernel, dim3(a.groups * a.Hkv), kWideThreads, C::SMEM, stream, 1, a, P);
@@ -804,9 +815,11 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_tree_wide(int dtype, int D, const DecodeArgs& a, const DecodePlan& P, cudaStream_t stream) {
-  if (dtype == FP2_BF16 && D == 128) return run<1, 128>(a, P, stream);
-  if (dtype == FP2_BF16 && D == 64) return run<1, 64>(a, P, stream);
-  if (dtype == FP2_E4M3 && D == 128) return run<2, 128>(a, P, stream);
+  bool split = false;
+  for (int r = 0; r < P.num_seqs; ++r) split |= split_weights((P.q_off[r + 1] - P.q_off[r]) * a.G);
+  if (dtype == FP2_BF16 && D == 128) return split ? run<1, 128, true>(a, P, stream) : run<1, 128, false>(a, P, stream);
+  if (dtype == FP2_BF16 && D == 64) return split ? run<1, 64, true>(a, P, stream) : run<1, 64, false>(a, P, stream);
+  if (dtype == FP2_E4M3 && D == 128) return run<2, 128, false>(a, P, stream);
   return cudaErrorInvalidValue;
 }
 

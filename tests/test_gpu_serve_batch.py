@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import serve_ref as R
-from tests.test_gpu_serve import Batch
+from tests.test_gpu_serve import Batch, _status, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -18,11 +18,11 @@ def _need_gpu():
     build.build()
 
 
-class Fine(Batch):
-    """Held to two bf16 halves of a weight whatever the batch (e4m3: f16)."""
-
-    def p_half(self):
-        return {"bf16": R.HALF["bf16"] ** 2, "e4m3": R.HALF["f16"], "f32": 0.0}[self.dtype]
+def _half(b, r):
+    """Half a step of the weights of sequence r, from its own rows: bf16 twice (hi + lo) up to 128, once above; f16."""
+    if b.dtype == "e4m3":
+        return R.HALF["f16"]
+    return R.HALF["bf16"] ** 2 if b.qlens[r] * b.hq // b.hkv <= 128 else R.HALF["bf16"]
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128)])
@@ -35,6 +35,12 @@ class Fine(Batch):
 ])
 def test_precision_does_not_depend_on_the_batch(dtype, d, hq, hkv, lens, qlens):
     for gain in (1.0, 3.0):                      # many weights that count, and few
-        b = Fine(dtype, d, hq, hkv, 64, lens, qlens, "tree", seed=33, gain=gain)
+        b = Batch(dtype, d, hq, hkv, 64, lens, qlens, "tree", seed=33, gain=gain)
         b.attend()
-        b.check()
+        assert _status(b.scratch) == (0, 0)
+        for r, n in enumerate(lens):
+            c = slice(b.cu[r], b.cu[r + 1])
+            o, l, mag, top = R.attend(*b.values(r), b.scale, b.vis[r])
+            b_out, b_lse = R.attend_bounds(o, l, mag, top, d, n, _half(b, r))
+            _within(R.f64(b.out[c]), o, b_out, f"out of sequence {r}")
+            _within(R.f64(b.lse[:, c]), l, b_lse, f"lse of sequence {r}")
