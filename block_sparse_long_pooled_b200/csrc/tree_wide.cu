@@ -64,9 +64,11 @@ struct Wide {
   static constexpr uint32_t IDESC_S = make_idesc(FMT_QK, FMT_QK, 0, 0, 128, TILE);
   static constexpr uint32_t IDESC_PV = make_idesc(FMT_PV, FMT_PV, 0, 1, 128, D);
   static constexpr float LAZY = 8.f;
-  // f16 holds 2^-14 with all its bits: a factor of 2^4 keeps small weights away from the subnormals,
-  // and 2^(4 + LAZY) far below the largest value.
-  static constexpr float P_BIAS = E4 ? 4.f : 0.f;
+  // f16 holds 2^-14 with all its bits and 2^16 not at all: a factor of 2^7 keeps weights down to 2^-21 of the largest
+  // away from the subnormals, and 2^(7 + LAZY), the most a weight can be, below the end.  (With 2^4, weights of
+  // 2^-27 beside a large one whose value is 0 were off by 1 %.)
+  static constexpr float P_BIAS = E4 ? 7.f : 0.f;
+  static_assert(P_BIAS + LAZY <= 15.f, "weights are f16");
   static constexpr int OFF_Q = 0;                              // [2] M tiles
   static constexpr int OFF_K = 2 * Q_BYTES;                    // [K_STAGES]
   static constexpr int OFF_V = OFF_K + K_STAGES * KV_BYTES;    // [V_STAGES]

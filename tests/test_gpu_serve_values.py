@@ -86,3 +86,11 @@ def test_a_score_that_is_nan_makes_row_and_lse_nan(dtype, d, hq, hkv, n, qlen):
         g = hq // hkv
         assert torch.isnan(b.lse[:g]).all() and torch.isfinite(b.lse[g:]).all(), (j0, j1)
         assert torch.isnan(b.out[:, :g].float()).all() and torch.isfinite(b.out[:, g:].float()).all(), (j0, j1)
+
+
+def test_small_weights_beside_a_large_one_whose_value_is_zero():
+    """e4m3, more than 16 rows: weights are f16, and what the small ones add up to has to keep its bits too."""
+    from tests.test_gpu_serve import Batch
+    b = Batch("e4m3", 128, 160, 5, 128, (3, 8, 1, 8, 9), (3, 8, 1, 8, 9), "tree", seed=602286, rows_over=7, joined=True, gain=4.0)
+    b.attend()
+    b.check()
