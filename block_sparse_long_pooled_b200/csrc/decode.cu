@@ -13,8 +13,8 @@
 // them: 16 rows are far below the 128 of a tcgen05 tile, and on that path the same calls were slower (three
 // short requests 21 us against 15, a batch of 64 263 us against 247, when that was compared).
 //
-// Measured: 64 requests of 0.5K to 16K bf16 keys, one token each, 241 us, 6.0 TB/s (220 us at the copy's
-// rate); three requests of 190 to 1000 keys 11 us, where the trips to memory one after another count:
+// Measured: 64 requests of 0.5K to 16K bf16 keys, one token each, 243 to 258 us, 5.6 to 6.0 TB/s (221 us at the
+// copy's rate), as many e4m3 keys 217 us (114); three requests of 190 to 1000 keys 11 us, where the trips to memory one after another count:
 // lengths, tile, statistics of the pieces, their rows.
 #include "decode_device.cuh"
 
@@ -127,7 +127,7 @@ struct Tree {
   static constexpr int RAW = (BUDGET - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = RAW > 8 ? 8 : RAW;
   static constexpr int SMEM = FIXED + STAGES * STAGE_BYTES;
-  // P is held in bf16 against a bf16 V.  Its rounding (2^-9 of each weight) would be as large as the
+  // P is held in bf16 against a bf16 V.  Its rounding (up to 2^-8 of each weight) would be as large as the
   // output's own; few rows leave the tensor cores idle, so a second product adds the remainder
   // P - bf16(P), which costs nothing measurable (a batch of 64 requests: 246.7 us with it, 247.7 without).
   static constexpr bool SPLIT_P = DT == 1;

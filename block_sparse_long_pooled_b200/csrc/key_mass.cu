@@ -11,7 +11,7 @@
 // Units as in decode.cu: (sequence, key tile of 128), weighted by the sequence's passes.  Warps: 0-3 and
 // 4-7 take the even and the odd tiles out of tensor memory; 8 loads K; 9 issues the products; 10 and 11
 // bring Q, -lse and the masks of the next pass into the second of two buffers while the current one is
-// worked on.  Measured: 32 tokens by 4 heads over 64K bf16 keys, 8 KV heads, 31 to 34 us (21 us of bytes);
+// worked on.  Measured: 32 tokens by 4 heads over 64K bf16 keys, 8 KV heads, 35 us (21 us of bytes);
 // one token of 32 sequences over 200 to 8K e4m3 keys 28 us (14 us of bytes), of which 17 in the tiles at
 // 5.3 TB/s and the rest before the first and after the last.
 #include "decode_device.cuh"

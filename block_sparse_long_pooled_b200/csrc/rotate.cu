@@ -21,9 +21,11 @@
 // each group of d / 16 lanes has a token of its own, so that a warp's work on one token (angles, factors,
 // addresses) serves two to eight; with few tokens the heads are spread over more warps instead (run_rotate).
 //
-// Measured: 64K tokens of 32 + 4 + 4 heads, norms, bf16 to e4m3 pages: 166 us, 6.1 TB/s (154 us at the
-// copy's rate; 178 us with a token a warp).  Eight tokens: 2.9 us in a graph, 4 to 5 us by call, which is the
-// host's time.
+// Measured: 64K tokens of 32 + 4 + 4 heads, norms, bf16 to e4m3 pages: 193 us, 5.2 TB/s (154 us at the copy's
+// rate; on one machine 166, where a token a warp took 178).  32K of them bf16 to bf16: 104 us (102).  Eight
+// tokens: 2.9 us in a graph, 4 us by call, which is the host's time.  f32 heads and interleaved bf16 pairs take
+// 1.8 to 2 times the bytes' time (61K tokens of 3 f32 heads 29 us, 14.5 of bytes): a lane's 8 values are 32 bytes,
+// or half of its 32, copied and stored 16 at a time, so that every sector moves twice.
 #include "fp2_device.cuh"
 #include "serve_kernels.h"
 

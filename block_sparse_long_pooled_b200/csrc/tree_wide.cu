@@ -13,12 +13,12 @@
 // rescaled in TMEM), and writes P over S in TMEM; O += P V.  A stream has two buffers of 64 columns:
 // S(j + 1) is computed while the softmax works on S(j).  With one buffer of 128 keys the exponentials stood
 // still for the products of every tile: 299 us for eight trees of 33 to 64 tokens by 8 heads on an e4m3
-// cache of 9K to 33K keys, now 148 (658 TFLOP/s).  There a pair's tile takes about 2,300 cycles.  The
+// cache of 9K to 33K keys, now 137 to 157 (620 to 710 TFLOP/s).  A pair's tile takes about 2,800 cycles of it.  The
 // exponentials (16 a cycle and SM) would need 1,024 of them and the products 900; taking either away saves
 // little, and half of them on the FMA pipe cost 10 us.  What bounds it is the chain: some 1,600 cycles in
 // which a stream's issuing warp waits, issues and commits S and O, and the softmax's loads, votes and
 // barriers around its arithmetic.  With few rows the cache's bytes bound the call: 7 tokens by 4 heads at
-// 128K bf16 keys 98 us, 82 of them in the tiles, at 6.5 TB/s.
+// 128K bf16 keys 96 to 116 us, 82 of them in the tiles.
 //
 // P in bf16 is off by up to 2^-8 of each weight, as much as the output's own rounding.  For sequences of up to
 // 128 rows, where the cache's bytes bound the call, a second product adds P - bf16(P) (2^-16), for which S has

@@ -300,7 +300,8 @@ typedef struct {
 
 /* Rotate: x' = norm(x) per head, pairs of the first rotary_dim values turn by their angle, V passes
  * through; one rounding, to out_dtype (E4M3 saturates at 448).  Angles are exact at any int32
- * position (no fp32 product of position and frequency).  An output may be its own input (same
+ * position (no fp32 product of position and frequency).  The sum of a head's squares is fp32: with a norm,
+ * a head whose squares pass its range comes out as zeros.  An output may be its own input (same
  * pointer, stride and type; K and V without slots); otherwise outputs must not overlap inputs.  Slots that
  * are >= 0 must be distinct.  status_dev: device word that FP2_DEV_* bits are OR-ed into, or NULL;
  * not cleared.  No scratch. */
@@ -333,7 +334,9 @@ FP2_API fp2_status fp2_decode_workspace(const fp2_decode* decode, size_t* scratc
  * not see have no influence on it, whatever their values (NaN included); an infinite or NaN value of a
  * key that it does see makes that element infinite or NaN.  The kernel goes by the batch's longest draft
  * (up to 16 query rows per KV head, or more), so a long draft can make short ones beside it slower; a
- * sequence's precision does not depend on the others. */
+ * sequence's precision goes by its own rows.  Sums and statistics are fp32; a weight is rounded for its
+ * product with V to 2^-16 over a BF16 cache (2^-8 in sequences of more than 128 rows per KV head), to
+ * 2^-11 over an E4M3 one, not at all over F32. */
 FP2_API fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void* scratch,
                                    size_t scratch_bytes, fp2_stream_t stream);
 
