@@ -336,7 +336,7 @@ FP2_API fp2_status fp2_decode_workspace(const fp2_decode* decode, size_t* scratc
  * (up to 16 query rows per KV head, or more), so a long draft can make short ones beside it slower; a
  * sequence's precision goes by its own rows.  Sums and statistics are fp32; a weight is rounded for its
  * product with V to 2^-16 over a BF16 cache (2^-8 in sequences of more than 128 rows per KV head), to
- * 2^-11 over an E4M3 one, not at all over F32. */
+ * 2^-11 over an E4M3 one (or 2^-32 of the row's largest weight, if that is more), not at all over F32. */
 FP2_API fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* lse, void* scratch,
                                    size_t scratch_bytes, fp2_stream_t stream);
 
