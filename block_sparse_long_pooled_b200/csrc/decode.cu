@@ -14,8 +14,8 @@
 // short requests 21 us against 15, a batch of 64 263 us against 247, when that was compared).
 //
 // Measured: 64 requests of 0.5K to 16K bf16 keys, one token each, 243 to 258 us, 5.6 to 6.0 TB/s (221 us at the
-// copy's rate), as many e4m3 keys 217 us (114); three requests of 190 to 1000 keys 11 us, where the trips to memory one after another count:
-// lengths, tile, statistics of the pieces, their rows.
+// copy's rate), as many e4m3 keys 217 us (114); three requests of 190 to 1000 keys 11 us, where the trips to
+// memory one after another count: lengths, tile, statistics of the pieces, their rows.
 #include "decode_device.cuh"
 
 namespace fp2 {

@@ -9,12 +9,13 @@
 // for the softmax, a thread one value of d and half the rows for P V.  K and V tiles come by cp.async, the
 // next while the current one is worked on; up to 4 rows three CTAs share an SM, above that two.
 //
-// What bounds it: with up to 4 rows per KV head HBM nearly (537 MB, 16 sequences of 8192 keys, 8 KV heads:
-// 104 to 113 us, 4.7 to 5.2 TB/s; the instance for 16 rows took 260 us there, two CTAs with room for 16 rows 146 us, a page id
-// read only when its tile is due 114 us).  With more rows the reads of Q, P and K from shared memory, one of
-// 16 bytes for two packed FMAs (the FMA pipe is at a quarter of its rate): 193 us for as many bytes and 8 rows, 72 us for 134 MB
-// and 16 rows, 245 us for 134 MB and 64 rows, which are four passes over K and V.  The weights: 268 MB of K and 4 rows in
-// 81 us (3.3 TB/s); a thread's K row is read 16 bytes at a time, so that L1 serves every second access.
+// What bounds it: with up to 4 rows per KV head HBM nearly (537 MB, 16 sequences of 8192 keys, 8 KV heads: 104 to
+// 113 us, 4.7 to 5.2 TB/s; the instance for 16 rows took 260 us there, two CTAs with room for 16 rows 146 us, a
+// page id read only when its tile is due 114 us).  With more rows the reads of Q, P and K from shared memory, one
+// of 16 bytes for two packed FMAs (the FMA pipe is at a quarter of its rate): 193 us for as many bytes and 8 rows,
+// 72 us for 134 MB and 16 rows, 245 us for 134 MB and 64 rows, which are four passes over K and V.  The weights:
+// 268 MB of K and 4 rows in 81 us (3.3 TB/s); a thread's K row is read 16 bytes at a time, so that L1 serves every
+// second access.
 #include "decode_device.cuh"
 
 namespace fp2 {

@@ -8,28 +8,26 @@
 //                                 index s mod 2, and their results are merged in shared memory.
 // A pair takes twice a parity tile's time, so a unit is an (M tile, key tile).
 //
-// Per key tile and stream: S = Q K^T into TMEM; one thread per row takes the row's 64 scores into
-// registers, masks them, raises the running maximum only when it grew by more than 2^8 (then O is
-// rescaled in TMEM), and writes P over S in TMEM; O += P V.  A stream has two buffers of 64 columns:
-// S(j + 1) is computed while the softmax works on S(j).  With one buffer of 128 keys the exponentials stood
-// still for the products of every tile: 299 us for eight trees of 33 to 64 tokens by 8 heads on an e4m3
-// cache of 9K to 33K keys, now 137 to 157 (620 to 710 TFLOP/s).  A pair's tile takes about 2,800 cycles of it.  The
-// exponentials (16 a cycle and SM) would need 1,024 of them and the products 900; taking either away saves
-// little, and half of them on the FMA pipe cost 10 us.  What bounds it is the chain: some 1,600 cycles in
-// which a stream's issuing warp waits, issues and commits S and O, and the softmax's loads, votes and
-// barriers around its arithmetic.  With few rows the cache's bytes bound the call: 7 tokens by 4 heads at
-// 128K bf16 keys 96 to 116 us, 82 of them in the tiles.
+// Per key tile and stream: S = Q K^T into TMEM; one thread per row takes the row's 64 scores into registers, masks
+// them, raises the running maximum only when it grew by more than 2^8 (then O is rescaled in TMEM), and writes P
+// over S in TMEM; O += P V.  A stream has two buffers of 64 columns: S(j + 1) is computed while the softmax works
+// on S(j).  With one buffer of 128 keys the exponentials stood still for the products of every tile: 299 us for
+// eight trees of 33 to 64 tokens by 8 heads on an e4m3 cache of 9K to 33K keys, now 137 to 157 (620 to 710
+// TFLOP/s).  A pair's tile takes about 2,800 cycles of it.  The exponentials (16 a cycle and SM) would need 1,024
+// of them and the products 900; taking either away saves little, and half of them on the FMA pipe cost 10 us.
+// What bounds it is the chain: some 1,600 cycles in which a stream's issuing warp waits, issues and commits S and
+// O, and the softmax's loads, votes and barriers around its arithmetic.  With few rows the cache's bytes bound the
+// call: 7 tokens by 4 heads at 128K bf16 keys 96 to 116 us, 82 of them in the tiles.
 //
-// P in bf16 is off by up to 2^-8 of each weight, as much as the output's own rounding.  For sequences of up to
-// 128 rows, where the cache's bytes bound the call, a second product adds P - bf16(P) (2^-16), for which S has
-// the columns: 7 tokens by 4 heads at 128K bf16 keys take 96 us with it, 91 without.  Above 128 rows, where
-// products and softmax do, P stays single: eight trees of 33 to 64 tokens by 8 heads on a bf16 cache of 9K to
-// 33K keys take 147 us, 161 with both.  The choice goes by the sequence's own rows: by the batch's longest
-// draft, a sequence's precision would depend on its neighbours.  e4m3: P is f16, and V is widened to f16 in shared memory by a warpgroup
-// of its own (the products of kind f16 want both operands of one type, and e4m3 weights would keep 4
-// bits).  That warpgroup also clears the rows of V that hold no key, and the elements of a drafted
-// key that are not finite (0 x NaN is NaN for rows that do not see the key); the epilogue adds those
-// back to the rows that do.
+// P in bf16 is off by up to 2^-8 of each weight, as much as the output's own rounding.  For sequences of up to 128
+// rows, where the cache's bytes bound the call, a second product adds P - bf16(P) (2^-16), for which S has the
+// columns: 7 tokens by 4 heads at 128K bf16 keys take 96 us with it, 91 without.  Above 128 rows, where products
+// and softmax do, P stays single: eight trees of 33 to 64 tokens by 8 heads on a bf16 cache of 9K to 33K keys take
+// 147 us, 161 with both.  The choice goes by the sequence's own rows: by the batch's longest draft, a sequence's
+// precision would depend on its neighbours.  e4m3: P is f16, and V is widened to f16 in shared memory by a
+// warpgroup of its own (the products of kind f16 want both operands of one type, and e4m3 weights would keep 4
+// bits).  That warpgroup also clears the rows of V that hold no key, and the elements of a drafted key that are
+// not finite (0 x NaN is NaN for rows that do not see the key); the epilogue adds those back to the rows that do.
 //
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1; 8 producer; 9, 10 MMA issuers of stream 0 and 1;
 // 12-15 V.  TMEM: S0 | S1 | O0 | O1, 128 columns each.

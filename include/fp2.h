@@ -344,9 +344,9 @@ FP2_API fp2_status fp2_tree_attend(const fp2_decode* decode, void* out, float* l
  * heads of its group, added to a decayed earlier sum:
  *   mass_out[r][g][j] = decay * mass_in[r][g][j] + sum_{h of g, t sees j} exp(q_t,h . k_j scale - lse[h][t])
  * mass: [num_seqs, Hkv, mass_stride] f32, mass_stride >= max_kv_len; mass_in may be NULL (zero) or
- * mass_out itself, and must not overlap it otherwise.  mass_len: device [num_seqs], how many keys mass_in covers (later ones count as
- * zero), or NULL: kv_len.  lse as fp2_tree_attend writes it.  Entries from kv_len on are left alone.
- * V is not read (cache.v may be NULL). */
+ * mass_out itself, and must not overlap it otherwise.  mass_len: device [num_seqs], how many keys
+ * mass_in covers (later ones count as zero), or NULL: kv_len.  lse as fp2_tree_attend writes it.
+ * Entries from kv_len on are left alone.  V is not read (cache.v may be NULL). */
 FP2_API fp2_status fp2_key_mass(const fp2_decode* decode, const float* lse, const float* mass_in, float* mass_out,
                                 int64_t mass_stride, const int32_t* mass_len, float decay, void* scratch,
                                 size_t scratch_bytes, fp2_stream_t stream);
