@@ -364,12 +364,18 @@ def alloc_pooled(ws: fp2_workspace, problem: Problem, device):
 
 
 def pooled_struct(t: dict) -> fp2_pooled:
-    """fp2_pooled from a dict of tensors (qbar, kbar, vbar, kbar_mma, vbar_mma and, for E4M3, v16)."""
-    return fp2_pooled(*(_ptr(t.get(k)) for k in ("qbar", "kbar", "vbar", "kbar_mma", "vbar_mma", "v16")))
+    """fp2_pooled from a dict of tensors (qbar, kbar, vbar, kbar_mma, vbar_mma and, for E4M3, v16), which it keeps
+    alive."""
+    s = fp2_pooled(*(_ptr(t.get(k)) for k in ("qbar", "kbar", "vbar", "kbar_mma", "vbar_mma", "v16")))
+    s.keep = tuple(t.values())
+    return s
 
 
 def index_struct(row_ptr, col_idx) -> fp2_index:
-    return fp2_index(_ptr(row_ptr), _ptr(col_idx), int(col_idx.numel()))
+    """fp2_index of two tensors, which it keeps alive."""
+    s = fp2_index(_ptr(row_ptr), _ptr(col_idx), int(col_idx.numel()))
+    s.keep = (row_ptr, col_idx)
+    return s
 
 
 def alloc_index(ws: fp2_workspace, device):
